@@ -19,6 +19,10 @@ Three operations, each a hand-written HIP kernel behind the C-ABI of ``include/b
 are exact: the pages state that the soft codeword is differentiable without approximation in the weights and in the
 trellis parameters (Technical Summary, "Core Mechanism").
 
+The layer that these weights belong to, and their update, are in ``layer``: ``fp8_block_quantize``,
+``fp8_block_matmul``, ``fp8_linear`` (autograd) and ``fp8_linear_quantized`` multiply by block-quantized 8-bit weights,
+and ``orthogonalize`` turns the gradient of the weights into an orthogonalized update.
+
 ``temperature_schedule`` gives the annealing sequence T0 -> T_end for a QAT run (host-side, see ``anneal``).
 
 Trellis variants: ``k`` (bits shifted in per step) may be 1 to 4 for every operation.  A codebook of shape [2^L, V]
@@ -38,7 +42,8 @@ from .anneal import temperature_schedule
 
 __all__ = ["soft_codeword", "soft_codeword_noalloc", "soft_codeword_grad", "soft_codeword_grad_codebook", "viterbi_hard_code",
            "viterbi_tail_biting", "soft_codeword_tail_biting", "soft_codeword_grad_tail_biting", "soft_quantize",
-           "temperature_schedule", "workspace_bytes", "BCJRError", "abi"]
+           "temperature_schedule", "workspace_bytes", "BCJRError", "abi", "fp8_block_quantize", "fp8_block_matmul",
+           "fp8_linear", "fp8_linear_quantized", "orthogonalize"]
 
 
 class BCJRError(RuntimeError):
@@ -355,3 +360,7 @@ def soft_quantize(w: torch.Tensor, codebook: torch.Tensor, L: int, k: int = 2, T
     [B, n V]); autograd runs the exact gradient kernels.  ``checkpoint`` runs the forward and backward calls with
     the smallest workspaces (checkpoint-and-recompute: about 2 sqrt(n) message rows per in-flight sequence)."""
     return _SoftQuantize.apply(w, codebook, L, k, T, boundary_state, checkpoint)
+
+
+# the layer's functions share the helpers above
+from .layer import fp8_block_matmul, fp8_block_quantize, fp8_linear, fp8_linear_quantized, orthogonalize  # noqa: E402

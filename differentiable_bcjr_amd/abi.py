@@ -20,6 +20,8 @@ BCJR_ERR_TEMP = -3
 BCJR_ERR_UNSUPPORTED = -4
 BCJR_ERR_WORKSPACE = -5
 BCJR_ERR_HIP = -6
+BCJR_ERR_LAYOUT = -7
+BCJR_ERR_SIZE = -8
 
 BCJR_OP_SOFT = 0
 BCJR_OP_GRAD = 1
@@ -32,6 +34,10 @@ BCJR_OP_GRAD_TAIL_BITING = 7
 
 BCJR_TB_EXACT = 0
 BCJR_TB_ROTATE = 1
+
+BCJR_TYPE_F32 = 0
+BCJR_TYPE_BF16 = 1
+BCJR_TYPE_F16 = 2
 
 BCJR_NOALLOC_SCRATCH_BYTES = 256 << 20
 
@@ -65,6 +71,11 @@ _SIGNATURES = {
     "bcjr_workspace_bytes_v": ([_i32, _i64, _i64, _i32, _i32, _i32], _sz),
     "bcjr_workspace_bytes_min": ([_i32, _i64, _i64, _i32, _i32, _i32], _sz),
     "bcjr_soft_codeword_noalloc": ([_vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp], _int),
+    "fp8_block_quantize": ([_vp, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp], _int),
+    "fp8_block_matmul": ([_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp], _int),
+    "orthogonalize": ([_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _f32, _f32, _f32, _f32, _vp, _i32, _vp, _sz,
+                       _vp], _int),
+    "orthogonalize_workspace_bytes": ([_i64, _i64, _i64, _i32], _sz),
     "bcjr_status_string": ([_i32], ctypes.c_char_p),
 }
 

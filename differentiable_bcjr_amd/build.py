@@ -18,7 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbcjr.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
-SOURCES = ["soft.hip", "grad.hip", "viterbi.hip", "tail_biting.hip", "general.hip", "bcjr_abi.cpp"]
+SOURCES = ["soft.hip", "grad.hip", "viterbi.hip", "tail_biting.hip", "general.hip", "fp8.hip", "orthogonalize.hip",
+           "bcjr_abi.cpp", "layer_abi.cpp"]
+HOST_SOURCES = ["bcjr_abi.cpp", "layer_abi.cpp"]   # the C-ABI: argument checks, workspace planning, dispatch
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -97,23 +99,26 @@ def asan_runtime() -> str:
 
 
 def build_sanitized(path: str) -> str:
-    """libbcjr.so with its C-ABI translation unit (every check and workspace plan) rebuilt with the host sanitizers,
+    """libbcjr.so with its C-ABI translation units (every check and workspace plan) rebuilt with the host sanitizers,
     linked with the kernels' objects of the last build into `path`; returns path."""
-    obj = path + ".abi.o"
-    cmd = [hipcc(), "-x", "hip", *HIPCC_FLAGS, *SANITIZE_HOST_FLAGS, "-c", os.path.join(CSRC, "bcjr_abi.cpp"), "-o",
-           obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed on bcjr_abi.cpp:\n{r.stdout}\n{r.stderr}")
-    objs = [obj if s == "bcjr_abi.cpp" else os.path.join(BUILD_DIR, s + ".o") for s in SOURCES]
-    missing = [o for o in objs if not os.path.exists(o)]
+    objs = {s: os.path.join(BUILD_DIR, s + ".o") for s in SOURCES}
+    for src in HOST_SOURCES:
+        objs[src] = f"{path}.{src}.o"
+        cmd = [hipcc(), "-x", "hip", *HIPCC_FLAGS, *SANITIZE_HOST_FLAGS, "-c", os.path.join(CSRC, src), "-o",
+               objs[src]]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"hipcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+    missing = [o for o in objs.values() if not os.path.exists(o)]
     if missing:
         raise RuntimeError(f"build() first: missing {missing}")
     r = subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-Xarch_host", "-fsanitize=address",
-                        "-Xarch_host", "-fsanitize=undefined", *objs, "-o", path], capture_output=True, text=True)
+                        "-Xarch_host", "-fsanitize=undefined", *objs.values(), "-o", path], capture_output=True,
+                       text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.remove(obj)
+    for src in HOST_SOURCES:
+        os.remove(objs[src])
     return path
 
 

@@ -377,6 +377,11 @@ const char* bcjr_status_string(int32_t status) {
             return "BCJR_ERR_WORKSPACE: workspace NULL, misaligned or smaller than bcjr_workspace_bytes(); or, for "
                    "bcjr_soft_codeword_noalloc, one sequence needs more than the library's static scratch holds";
         case BCJR_ERR_HIP: return "BCJR_ERR_HIP: the HIP runtime reported a launch error";
+        case BCJR_ERR_LAYOUT:
+            return "BCJR_ERR_LAYOUT: rows closer together than they are long, or an 8-bit matrix whose base or row "
+                   "distance is no multiple of 16 bytes";
+        case BCJR_ERR_SIZE:
+            return "BCJR_ERR_SIZE: a size, step count, block size or element type that the entry point does not take";
         default: return "BCJR: unknown status";
     }
 }

@@ -1,0 +1,464 @@
+// fp8.hip -- 8-bit block quantization (e4m3 codes, one float32 scale per block of 128) and the product of two
+// matrices held that way.
+#include "bcjr.h"
+
+#include <hip/hip_bf16.h>
+#include <hip/hip_fp16.h>
+
+#include "layer_args.hpp"
+#include "mfma_tile.hpp"
+
+namespace bcjr {
+namespace {
+
+// ------------------------------------------------------------------------------------------------ quantization
+//
+// A block's scale is s = max(amax / 448, 2^-126) and its codes are e4m3(x / s), with both divisions as multiplications
+// by float32 constants (fl(1/448) and fl(1/s)), each product rounded to float32 before the rounding to e4m3 (to the
+// nearest, ties to even): elementary float32 operations in a fixed order, so any implementation of them gives the same
+// codes.  The floor 2^-126 keeps 1/s finite; it also makes a block of zeros quantize to zeros.  amax is taken on the
+// bit patterns of |x|, where Inf and NaN sort above every number: they reach the scale and so the block's results.
+
+constexpr float kInvMax = 1.0f / 448.0f;   // 448: the largest e4m3 number
+constexpr float kMinScale = 1.17549435e-38f;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__hip_bfloat16 x) {
+    return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, x) << 16);
+}
+__device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
+
+// 8 elements from p on, the first `count` of them present (the rest 0).  `wide`: all 8 are, on a 16-byte boundary.
+template <class T>
+__device__ __forceinline__ void load8(const T* p, int count, bool wide, float (&v)[8]) {
+    if (wide) {
+        constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+        for (int j = 0; j < 8; j += kPer) {
+            const v4i w = *(const v4i*)(p + j);
+            T e[kPer];
+            __builtin_memcpy(e, &w, 16);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) v[j + i] = to_f32(e[i]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < count ? to_f32(p[j]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    return m;
+}
+
+__device__ __forceinline__ float block_scale(uint32_t amax) {
+    const float s = __uint_as_float(amax) * kInvMax;
+    return s < kMinScale ? kMinScale : s;   // NaN stays
+}
+
+// Four codes in the bytes of one word.  |x r| is at most 448 (1 + 2^-23) unless it is NaN, and the instruction rounds
+// that to 448.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float r) {
+    return make_uint2(codes4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), codes4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+}
+
+__device__ __forceinline__ void store8(uint8_t* p, int count, uint2 w) {
+    if (count >= 8) {
+        *(uint2*)p = w;
+    } else {
+        for (int j = 0; j < count; ++j) p[j] = (uint8_t)((j < 4 ? w.x >> (8 * j) : w.y >> (8 * (j - 4))) & 0xff);
+    }
+}
+
+// Rows alone: 16 lanes hold one row's block of 128, eight elements each.  Bound by memory.
+constexpr int kRowsPerGroup = 16;
+
+template <class T>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int col_blocks, int wide) {
+    const int t = threadIdx.x;
+    const int cb = blockIdx.x % col_blocks;
+    const int64_t row = (int64_t)(blockIdx.x / col_blocks) * kRowsPerGroup + (t >> 4);
+    const int64_t col = (int64_t)cb * 128 + (t & 15) * 8;
+    const bool have = row < a.rows;
+    const int64_t left = have ? a.cols - col : 0;
+    float v[8] = {};
+    if (left > 0) load8((const T*)a.x + row * a.ld_x + col, (int)min(left, (int64_t)8), wide && left >= 8, v);
+    uint32_t m = max8(v);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    const float s = block_scale(m);
+    if (left > 0) store8(a.q + row * a.ld_q + col, (int)min(left, (int64_t)8), codes8(v, 1.0f / s));
+    if (have && (t & 15) == 0) a.scale[(int64_t)cb * a.rows + row] = s;
+}
+
+// A tile of 128 x 128: square blocks, and any quantization that also writes the transpose.  Thread t holds eight
+// columns of eight consecutive rows, so both orientations leave it as words of eight codes; the transposed codes pass
+// through LDS to be written in whole 128-byte lines.
+template <class T, bool kSquare, bool kTransposed>
+__global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int col_blocks, int row_blocks,
+                                                            int wide) {
+    __shared__ uint32_t col_max[4][128];
+    __shared__ __align__(16) uint8_t codes_t[kTransposed ? 128 * 128 : 16];
+    const int t = threadIdx.x;
+    const int i = t & 15, band = t >> 4;   // columns 8 i .. 8 i + 7, rows 8 band .. 8 band + 7 of the tile
+    const int cb = blockIdx.x % col_blocks, rb = blockIdx.x / col_blocks;
+    const int64_t row0 = (int64_t)rb * 128, col0 = (int64_t)cb * 128;
+    const int64_t col = col0 + i * 8;
+    const int64_t rows_left = a.rows - (row0 + band * 8);
+    const int64_t cols_left = a.cols - col;
+    float v[8][8] = {};
+    if (cols_left > 0) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            if (p < rows_left)
+                load8((const T*)a.x + (row0 + band * 8 + p) * a.ld_x + col, (int)min(cols_left, (int64_t)8),
+                      wide && cols_left >= 8, v[p]);
+    }
+
+    float inv_square = 0.0f;
+    if constexpr (kSquare) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) m = max(m, max8(v[p]));
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        if ((t & 63) == 0) col_max[t >> 6][0] = m;
+        __syncthreads();
+        m = max(max(col_max[0][0], col_max[1][0]), max(col_max[2][0], col_max[3][0]));
+        const float s = block_scale(m);
+        inv_square = 1.0f / s;
+        if (t == 0) {
+            a.scale[(int64_t)cb * row_blocks + rb] = s;
+            if constexpr (kTransposed) a.scale_t[(int64_t)rb * col_blocks + cb] = s;
+        }
+    }
+
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        float r = inv_square;
+        if constexpr (!kSquare) {
+            uint32_t m = max8(v[p]);
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+            const float s = block_scale(m);
+            r = 1.0f / s;
+            if (i == 0 && p < rows_left) a.scale[(int64_t)cb * a.rows + row0 + band * 8 + p] = s;
+        }
+        if (p < rows_left && cols_left > 0)
+            store8(a.q + (row0 + band * 8 + p) * a.ld_q + col, (int)min(cols_left, (int64_t)8), codes8(v[p], r));
+    }
+
+    if constexpr (kTransposed) {
+        float inv[8];
+        if constexpr (kSquare) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) inv[j] = inv_square;
+        } else {
+            uint32_t m[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m[j] = 0;
+#pragma unroll
+                for (int p = 0; p < 8; ++p) m[j] = max(m[j], abs_bits(v[p][j]));
+                m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16));
+                m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32));
+            }
+            if ((t & 63) < 16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) col_max[t >> 6][i * 8 + j] = m[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = i * 8 + j;
+                const float s = block_scale(max(max(col_max[0][c], col_max[1][c]), max(col_max[2][c], col_max[3][c])));
+                inv[j] = 1.0f / s;
+                if (band == 0 && j < cols_left) a.scale_t[(int64_t)rb * a.cols + col + j] = s;
+            }
+        }
+        // column c's codes are 16 words of 8 rows; word `band` lies at band ^ (c / 8), which spreads the 16 columns
+        // that a step writes over the banks
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float r = inv[j];
+            const uint2 w = make_uint2(codes4(v[0][j] * r, v[1][j] * r, v[2][j] * r, v[3][j] * r),
+                                       codes4(v[4][j] * r, v[5][j] * r, v[6][j] * r, v[7][j] * r));
+            *(uint2*)(codes_t + (i * 8 + j) * 128 + ((band ^ i) * 8)) = w;
+        }
+        __syncthreads();
+        const int64_t rows_tile = a.rows - row0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int c = p * 32 + (t >> 3);
+            const int w = (t & 7) * 2;
+            if (col0 + c >= a.cols) continue;
+            const uint2 lo = *(const uint2*)(codes_t + c * 128 + ((w ^ (c >> 3)) * 8));
+            const uint2 hi = *(const uint2*)(codes_t + c * 128 + (((w + 1) ^ (c >> 3)) * 8));
+            uint8_t* out = a.q_t + (col0 + c) * a.ld_qt + row0 + w * 8;
+            const int64_t left = rows_tile - w * 8;
+            if (left >= 16) {
+                *(uint4*)out = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else if (left > 0) {
+                store8(out, (int)min(left, (int64_t)8), lo);
+                if (left > 8) store8(out + 8, (int)(left - 8), hi);
+            }
+        }
+    }
+}
+
+template <class T>
+hipError_t quantize(const QuantizeArgs& a, hipStream_t st) {
+    const int wide = ((uintptr_t)a.x % 16 == 0 && (a.ld_x * sizeof(T)) % 16 == 0) ? 1 : 0;
+    const int cb = (int)((a.cols + 127) / 128), rb = (int)((a.rows + 127) / 128);
+    if (a.block_rows == 1 && !a.q_t) {
+        const unsigned grid = (unsigned)cb * (unsigned)((a.rows + kRowsPerGroup - 1) / kRowsPerGroup);
+        quantize_rows_kernel<T><<<grid, 256, 0, st>>>(a, cb, wide);
+    } else {
+        const unsigned grid = (unsigned)cb * (unsigned)rb;
+        if (a.block_rows == 1)
+            quantize_tile_kernel<T, false, true><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+        else if (a.q_t)
+            quantize_tile_kernel<T, true, true><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+        else
+            quantize_tile_kernel<T, true, false><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+    }
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------------ product
+//
+// out[i][j] = sum over blocks B of sa[i][B] sb[j][B] sum over k in B of a[i][k] b[j][k].  A slab is one block, so each
+// MFMA (or four of the 16-bit kind) sums one block of one 16 x 16 tile from zero, and a float32 fused multiply-add with
+// the two scales' product moves it into the running sum.  The MFMA's row operand is b, so a lane holds four neighbouring
+// outputs of one row of a: one scale of a for each 16 rows, and a vector store.
+//
+// The 8-bit instruction aligns the products of eight neighbouring k to the largest of them and drops what lies more than
+// 13 bits below its leading bit (measured: 2^16 + 2^2 gives 2^16 within such a group, and a full float32 sum across
+// groups).  That is far below the rounding of a 16-bit result but not of a float32 one, so a float32 result is computed
+// with the 16-bit instruction on codes widened to halves, which hold every e4m3 number: exact products, float32 sums,
+// at half the rate.
+
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ _Float16 from_f32<_Float16>(float x) { return (_Float16)x; }
+template <>
+__device__ __forceinline__ __hip_bfloat16 from_f32<__hip_bfloat16>(float x) { return __float2bfloat16(x); }
+
+// The 32 codes of a fragment as 32 halves, for four 16x16x32 MFMAs.
+struct Halves {
+    v8h h[4];
+};
+
+__device__ __forceinline__ Halves widen(v8i codes) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    Halves out;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const v2h lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, false);
+        const v2h hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes[i], 1.0f, true);
+        out.h[i / 2][i % 2 * 4 + 0] = lo[0];
+        out.h[i / 2][i % 2 * 4 + 1] = lo[1];
+        out.h[i / 2][i % 2 * 4 + 2] = hi[0];
+        out.h[i / 2][i % 2 * 4 + 3] = hi[1];
+    }
+    return out;
+}
+
+__device__ __forceinline__ v4f block_product(const Halves& a, const Halves& b) {
+    v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[h], b.h[h], p, 0, 0, 0);
+    return p;
+}
+
+__device__ __forceinline__ v4f block_product(v8i a, v8i b) {
+    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
+}
+
+template <bool kWide>
+struct Fragment {
+    v8i v;
+    __device__ __forceinline__ void set(v8i codes) { v = codes; }
+};
+template <>
+struct Fragment<true> {
+    Halves v;
+    __device__ __forceinline__ void set(v8i codes) { v = widen(codes); }
+};
+
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N, bool kRowScales>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(ProductArgs a, int tiles_m, int tiles_n) {
+    constexpr int kWaves = WAVES_M * WAVES_N;
+    constexpr bool kWide = sizeof(T) == 4;
+    constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
+    static_assert(kRowScales || 128 % (BN / WAVES_N) == 0, "a wave's columns lie in one block of b");
+    __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kSlab];
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    int bm, bn;
+    banded_tile(xcd_order(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8, bm, bn);
+    const int m0 = bm * BM, n0 = bn * BN;
+    const uint8_t* pa = a.a + (int64_t)m0 * a.ld_a;
+    const uint8_t* pb = a.b + (int64_t)n0 * a.ld_b;
+    const int rows_a = a.m - m0, rows_b = a.n - n0;
+    const int slabs = (a.k + kSlab - 1) / kSlab;
+    const int r16 = lane & 15, g = lane >> 4;
+
+    auto fetch = [&](int s, uint8_t* to) {
+        const int left = a.k - s * kSlab;
+        if (left >= kSlab) {
+            fetch_slab<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, s * kSlab, to, wave, lane);
+            fetch_slab<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, s * kSlab, to + BM * kSlab, wave, lane);
+        } else {
+            fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, s * kSlab, left, to, wave, lane);
+            fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, s * kSlab, left, to + BM * kSlab, wave, lane);
+        }
+    };
+
+    const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
+    int ma[TM];   // rows of a whose scales this lane applies
+#pragma unroll
+    for (int i = 0; i < TM; ++i) ma[i] = min(m0 + wm0 + i * 16 + r16, a.m - 1);
+    const int sb_len = kRowScales ? a.n : (a.n + 127) / 128;
+    const int sb_at = kRowScales ? 0 : min((n0 + wn0) / 128, sb_len - 1);
+
+    v4f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // The scales of a slab are loaded ahead of the next slab's operands, a step before their use: loads complete in
+    // order, so a load behind the operands would be waited for with them.
+    float sa_next[TM], sb_next[TN][4];
+    auto fetch_scales = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa_next[i] = a.a_scale[(int64_t)s * a.m + ma[i]];
+        if constexpr (kRowScales) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sb_next[j][e] = a.b_scale[(int64_t)s * a.n + min(n0 + wn0 + j * 16 + g * 4 + e, a.n - 1)];
+        } else {
+            sb_next[0][0] = a.b_scale[(int64_t)s * sb_len + sb_at];
+        }
+    };
+    if (slabs > 0) {
+        fetch_scales(0);
+        fetch(0, lds[0]);
+    }
+    for (int s = 0; s < slabs; ++s) {
+        wait_loads();
+        __syncthreads();   // slab s is in LDS, and nobody reads the other buffer any more
+        float sa[TM], sb[TN][4];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = kRowScales ? sa_next[i] : sa_next[i] * sb_next[0][0];
+        if constexpr (kRowScales) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sb[j][e] = sb_next[j][e];
+        }
+        if (s + 1 < slabs) {
+            fetch_scales(s + 1);
+            fetch(s + 1, lds[(s + 1) & 1]);
+        }
+        const uint8_t* la = lds[s & 1];
+        const uint8_t* lb = la + BM * kSlab;
+        Fragment<kWide> fa[TM];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            v4i lo, hi;
+            read_fragment(la, wm0 + i * 16 + r16, g, lo, hi);
+            fa[i].set(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            v4i lo, hi;
+            read_fragment(lb, wn0 + j * 16 + r16, g, lo, hi);
+            Fragment<kWide> fb;
+            fb.set(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const v4f p = block_product(fb.v, fa[i].v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (kRowScales)
+                        acc[i][j][e] = fmaf(p[e] * sb[j][e], sa[i], acc[i][j][e]);
+                    else
+                        acc[i][j][e] = fmaf(p[e], sa[i], acc[i][j][e]);
+                }
+            }
+        }
+    }
+
+    T* out = (T*)a.out;
+    const bool wide = ((uintptr_t)out % (4 * sizeof(T)) == 0) && (a.ld_out % 4 == 0);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int m = m0 + wm0 + i * 16 + r16;
+        if (m >= a.m) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int n = n0 + wn0 + j * 16 + g * 4;
+            T e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e[x] = from_f32<T>(acc[i][j][x]);
+            T* to = out + (int64_t)m * a.ld_out + n;
+            if (wide && n + 4 <= a.n) {
+                __builtin_memcpy(__builtin_assume_aligned(to, 4 * sizeof(T)), e, sizeof(e));
+            } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (n + x < a.n) to[x] = e[x];
+            }
+        }
+    }
+}
+
+template <class T>
+hipError_t product(const ProductArgs& a, hipStream_t st) {
+    const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128;
+    const unsigned grid = (unsigned)tm * (unsigned)tn;
+    if (a.b_rows == 1)
+        product_kernel<T, 128, 128, 2, 2, true><<<grid, 256, 0, st>>>(a, tm, tn);
+    else
+        product_kernel<T, 128, 128, 2, 2, false><<<grid, 256, 0, st>>>(a, tm, tn);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const QuantizeArgs& a, hipStream_t st) {
+    switch (a.type) {
+        case BCJR_TYPE_F32: return quantize<float>(a, st);
+        case BCJR_TYPE_BF16: return quantize<__hip_bfloat16>(a, st);
+        default: return quantize<_Float16>(a, st);
+    }
+}
+
+hipError_t launch_fp8_product(const ProductArgs& a, hipStream_t st) {
+    switch (a.out_type) {
+        case BCJR_TYPE_F32: return product<float>(a, st);
+        case BCJR_TYPE_BF16: return product<__hip_bfloat16>(a, st);
+        default: return product<_Float16>(a, st);
+    }
+}
+
+}  // namespace bcjr

@@ -62,7 +62,11 @@ enum {
                                   unknown mode */
     BCJR_ERR_WORKSPACE = -5,   /* workspace NULL, not 256-byte aligned, or smaller than bcjr_workspace_bytes();
                                   bcjr_soft_codeword_noalloc: one sequence needs more than the static scratch */
-    BCJR_ERR_HIP = -6          /* the HIP runtime reported an error at launch */
+    BCJR_ERR_HIP = -6,         /* the HIP runtime reported an error at launch */
+    BCJR_ERR_LAYOUT = -7,      /* quantized layer and update: rows closer together than they are long, or an 8-bit
+                                  matrix whose base or row distance is no multiple of 16 bytes */
+    BCJR_ERR_SIZE = -8         /* quantized layer and update: a size, step count, block size or element type outside
+                                  the values that the entry point takes */
 };
 
 enum {
@@ -268,6 +272,68 @@ size_t bcjr_workspace_bytes_min(int32_t op, int64_t B, int64_t n, int32_t L, int
  */
 int bcjr_soft_codeword_noalloc(const float* w, const float* codebook, int64_t B, int64_t n, int32_t L, int32_t k,
                                float T, const int32_t* boundary_state, float* w_soft, float* log_z, void* stream);
+
+/*
+ * ---- A layer with quantized weights: 8-bit block-scaled products, and the orthogonalized update of its weights.
+ *
+ * These entry points take the soft or hard codeword where training and serving use it, as the weights of a linear
+ * layer, and turn the gradient of the weights into an update.  As above, every tensor pointer is a device pointer owned
+ * by the caller, nothing is allocated or synchronized, and every check but BCJR_ERR_HIP runs before any launch.  Row
+ * distances (ld_*) are in elements of the array.  Matrices with no rows or no columns are accepted and leave their
+ * outputs untouched (a product over k = 0 writes zeros).  Row counts, column counts and k are at most 2^30.
+ */
+enum { BCJR_TYPE_F32 = 0, BCJR_TYPE_BF16 = 1, BCJR_TYPE_F16 = 2 };
+
+/*
+ * Block quantization to 8-bit floating point (e4m3, the variant without infinities, largest number 448).  Columns are
+ * cut into blocks of 128 (the last may be shorter); a block is 128 columns of one row (block_rows = 1) or of 128 rows
+ * (block_rows = 128).  With amax the largest |x| of the block,
+ *   scale = max(fl(amax * fl(1/448)), 2^-126),   q = e4m3(fl(x * fl(1/scale))),
+ * every fl a rounding to float32 and e4m3 the rounding to the nearest code, ties to even, so q scale stands for x with
+ * an error of at most 2^-4 of |x|, or 2^-10 scale where |x| is under 2^-6 scale.  A block of zeros gives zeros.  An Inf
+ * in a block makes its scale Inf, a NaN NaN, and either makes every value of that block NaN.
+ * q is [rows, cols], its rows ld_q bytes apart, and scale [ceil(cols/128)][ceil(rows/block_rows)].  With q_t the
+ * transpose is quantized in the same pass: q_t [cols, rows], its rows ld_qt bytes apart, with blocks of 128 rows of x
+ * of one column, or of 128 columns (block_rows = 128: the same codes and scales), and scale_t
+ * [ceil(rows/128)][ceil(cols/block_rows)].  q_t and scale_t are given together or not at all.  q and q_t lie on 16-byte
+ * boundaries and ld_q, ld_qt are multiples of 16 (BCJR_ERR_LAYOUT); bytes between a row's end and the next row are left
+ * as they are.  type is one of BCJR_TYPE_*; another type or block_rows gives BCJR_ERR_SIZE.
+ */
+int fp8_block_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, int64_t ld_x, int32_t block_rows,
+                       void* q, int64_t ld_q, float* scale, void* q_t, int64_t ld_qt, float* scale_t, void* stream);
+
+/*
+ * Product of two block-quantized matrices: out[i, j] = sum_k a[i, k] b[j, k] over the values that the codes and scales
+ * stand for, out [m, n] of out_type with rows ld_out elements apart.  a [m, k] has a scale for each block of 128 of a
+ * row, a_scale [ceil(k/128)][m]; b [n, k] the same with b_block_rows = 1, or one for each 128 x 128 block,
+ * b_scale [ceil(k/128)][ceil(n/128)], with b_block_rows = 128.  A block is summed first and added to the running float32
+ * sum with one multiplication by its scales.  For a float32 result a block's products are exact and summed in float32.
+ * For a bfloat16 or float16 result the 8-bit matrix instruction sums it, which cuts the products of 8 neighbouring k
+ * 13 bits below the largest exponent among them (a relative error near 1e-4 on random data, under the result's own
+ * rounding).  a and b lie on 16-byte boundaries with ld_a, ld_b multiples of 16
+ * below 2^31 (BCJR_ERR_LAYOUT); bytes behind a row's k codes are not used.
+ */
+int fp8_block_matmul(const void* a, int64_t ld_a, const float* a_scale, const void* b, int64_t ld_b,
+                     const float* b_scale, int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* out,
+                     int32_t out_type, int64_t ld_out, void* stream);
+
+/*
+ * Orthogonalized update (Newton-Schulz iteration, the direction that the Muon optimizer takes): for each matrix G of a
+ * batch, X = G / (|G|_F + eps), then `steps` times
+ *   A = X X^T,  X <- a X + (b A + c A A) X,
+ * on the transpose when G has more rows than columns.  With a, b, c = 3.4445, -4.7750, 2.0315 five steps bring the
+ * singular values near 1.  g is [batch][rows, cols] of `type`, rows ld_g and matrices batch_g elements apart; out is
+ * contiguous, of out_type.  Sums are float32 (|G|_F: float64).  A float32 or float16 result is as near the exact
+ * iteration as one of float32 products; a bfloat16 result comes from products of operands rounded to 11 bits, whose
+ * error is below that of the result's own rounding.  The iterates must stay below 64 in |X| and 256 in |A| and
+ * |b A + c A A| (the usual coefficients keep them under 3); beyond that the result has Inf or NaN entries.  A NaN or Inf
+ * in G makes that matrix's result NaN.  1 <= steps <= 1000, 1 <= batch <= 65535, rows, cols <= 65536.
+ * Workspace: orthogonalize_workspace_bytes, 256-byte aligned (BCJR_ERR_WORKSPACE).
+ */
+int orthogonalize(const void* g, int32_t type, int64_t batch, int64_t rows, int64_t cols, int64_t ld_g, int64_t batch_g,
+                  int32_t steps, float a, float b, float c, float eps, void* out, int32_t out_type, void* workspace,
+                  size_t workspace_bytes, void* stream);
+size_t orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols, int32_t out_type);
 
 /* Static, NUL-terminated description of a status code. */
 const char* bcjr_status_string(int32_t status);
