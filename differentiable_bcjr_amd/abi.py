@@ -73,6 +73,8 @@ _SIGNATURES = {
     "bcjr_soft_codeword_noalloc": ([_vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp], _int),
     "fp8_block_quantize": ([_vp, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp], _int),
     "fp8_block_matmul": ([_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp], _int),
+    "fp8_linear_quantized": ([_vp, _i32, _i64, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _i64, _vp, _sz, _vp], _int),
+    "fp8_linear_quantized_workspace_bytes": ([_i64, _i64], _sz),
     "orthogonalize": ([_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _f32, _f32, _f32, _f32, _vp, _i32, _vp, _sz,
                        _vp], _int),
     "orthogonalize_workspace_bytes": ([_i64, _i64, _i64, _i32], _sz),

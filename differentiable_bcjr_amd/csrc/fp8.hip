@@ -381,22 +381,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
         }
         const uint8_t* la = lds[s & 1];
         const uint8_t* lb = la + BM * kSlab;
-        Fragment<kWide> fa[TM];
+        Fragment<kWide> fb[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[j].set(read_slab(lb, wn0 + j * 16 + r16, g));
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            v4i lo, hi;
-            read_fragment(la, wm0 + i * 16 + r16, g, lo, hi);
-            fa[i].set(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        }
+            Fragment<kWide> fa;
+            fa.set(read_slab(la, wm0 + i * 16 + r16, g));
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            v4i lo, hi;
-            read_fragment(lb, wn0 + j * 16 + r16, g, lo, hi);
-            Fragment<kWide> fb;
-            fb.set(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-#pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const v4f p = block_product(fb.v, fa[i].v);
+            for (int j = 0; j < TN; ++j) {
+                const v4f p = block_product(fb[j].v, fa.v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     if constexpr (kRowScales)
@@ -432,14 +426,160 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
     }
 }
 
+// ---- few rows
+//
+// With at most 16 rows of a the product is bound by reading b, once.  A wave takes 16 rows of b straight from memory
+// into the MFMA's operand (lane l: the 16-byte chunks l >> 4 and (l >> 4) + 4 of row l & 15, so one load covers whole
+// 64-byte sectors), the workgroup's waves share the slabs of those rows among them, four slabs of each in flight, and
+// their sums meet in LDS in a fixed order.  a either comes as codes or as numbers that are quantized in the operand's
+// registers: the four lanes of a row hold its whole block, so its largest entry is two lane exchanges away.
+
+// Chunk `at` .. at + 15 of a row of k codes, zeros behind its end.
+__device__ __forceinline__ v4i load_chunk(const uint8_t* row, int at, int k) {
+    if (at + 16 <= k) return *(const v4i*)(row + at);
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int b = 0; b < k - at; ++b) w[b >> 2] |= (uint32_t)row[at + b] << ((b & 3) * 8);
+    return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+}
+
+__device__ __forceinline__ v8i load_slab(const uint8_t* row, int at, int g, int k) {
+    return __builtin_shufflevector(load_chunk(row, at + g * 16, k), load_chunk(row, at + 64 + g * 16, k), 0, 1, 2, 3, 4,
+                                   5, 6, 7);
+}
+
+// The same chunks of a row of numbers, as codes; `scale` is the block's.
+template <class X>
+__device__ __forceinline__ v8i quantize_slab(const X* row, int at, int g, int k, bool have, bool wide, float& scale) {
+    float v[4][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const int from = at + (h >> 1) * 64 + g * 16 + (h & 1) * 8;
+        const int left = have ? k - from : 0;
+        if (left > 0) {
+            load8(row + from, min(left, 8), wide && left >= 8, v[h]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
+        }
+        m = max(m, max8(v[h]));
+    }
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    scale = block_scale(m);
+    const float r = 1.0f / scale;
+    v8i out;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const uint2 c = codes8(v[h], r);
+        out[h * 2] = (int)c.x;
+        out[h * 2 + 1] = (int)c.y;
+    }
+    return out;
+}
+
+constexpr int kFewRows = 16;
+constexpr int kAhead = 4;   // slabs whose loads a wave has in flight
+
+// X: the type of a's numbers, or uint8_t for codes.
+template <class T, class X, bool kRowScales>
+__global__ __launch_bounds__(1024) void few_rows_kernel(ProductArgs a, int wide) {
+    constexpr bool kWide = sizeof(T) == 4, kCodes = sizeof(X) == 1;
+    __shared__ float sums[16][256];
+    const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const int slabs = (a.k + kSlab - 1) / kSlab;
+    const uint8_t* b_row = a.b + (int64_t)min(n0 + r16, a.n - 1) * a.ld_b;
+    const bool have = r16 < a.m;
+    const X* a_row = (const X*)a.a + (int64_t)(have ? r16 : 0) * a.ld_a;
+    const int sb_len = kRowScales ? a.n : (a.n + 127) / 128;
+
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = wave; s0 < slabs; s0 += waves * kAhead) {
+        v8i fb[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = s0 + u * waves;
+            if (s < slabs) fb[u] = load_slab(b_row, s * kSlab, g, a.k);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int s = s0 + u * waves;
+            if (s >= slabs) break;
+            float sa = 0.0f;
+            v8i fa;
+            if constexpr (kCodes) {
+                fa = v8i{0, 0, 0, 0, 0, 0, 0, 0};
+                if (have) {
+                    fa = load_slab(a_row, s * kSlab, g, a.k);
+                    sa = a.a_scale[(int64_t)s * a.m + r16];
+                }
+            } else {
+                fa = quantize_slab(a_row, s * kSlab, g, a.k, have, wide != 0, sa);
+            }
+            Fragment<kWide> wa, wb;
+            wa.set(fa);
+            wb.set(fb[u]);
+            const v4f p = block_product(wb.v, wa.v);
+            const float* sb = a.b_scale + (int64_t)s * sb_len;
+            if constexpr (kRowScales) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e] * sb[min(n0 + g * 4 + e, a.n - 1)], sa, acc[e]);
+            } else {
+                const float both = sa * sb[n0 / 128];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], both, acc[e]);
+            }
+        }
+    }
+    // sums[wave][row of a][column]
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums[wave][r16 * 16 + g * 4 + e] = acc[e];
+    __syncthreads();
+    for (int o = threadIdx.x; o < a.m * 16; o += blockDim.x) {
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) v += sums[w][o];
+        if (n0 + (o & 15) < a.n) ((T*)a.out)[(int64_t)(o >> 4) * a.ld_out + n0 + (o & 15)] = from_f32<T>(v);
+    }
+}
+
+template <class T, class X>
+void few_rows(const ProductArgs& a, hipStream_t st) {
+    const int slabs = (a.k + kSlab - 1) / kSlab;
+    int waves = 1;   // as many as leave each about kAhead slabs
+    while (waves < 16 && waves * kAhead < slabs) waves *= 2;
+    const unsigned grid = (unsigned)((a.n + 15) / 16);
+    const int wide = (uintptr_t)a.a % 16 == 0 && (a.ld_a * sizeof(X)) % 16 == 0;
+    if (a.b_rows == 1)
+        few_rows_kernel<T, X, true><<<grid, waves * 64, 0, st>>>(a, wide);
+    else
+        few_rows_kernel<T, X, false><<<grid, waves * 64, 0, st>>>(a, wide);
+}
+
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N>
+void product_tiles(const ProductArgs& a, hipStream_t st) {
+    const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
+    const unsigned grid = (unsigned)tm * (unsigned)tn;
+    constexpr int kThreads = 64 * WAVES_M * WAVES_N;
+    if (a.b_rows == 1)
+        product_kernel<T, BM, BN, WAVES_M, WAVES_N, true><<<grid, kThreads, 0, st>>>(a, tm, tn);
+    else
+        product_kernel<T, BM, BN, WAVES_M, WAVES_N, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
+}
+
 template <class T>
 hipError_t product(const ProductArgs& a, hipStream_t st) {
-    const int tm = (a.m + 127) / 128, tn = (a.n + 127) / 128;
-    const unsigned grid = (unsigned)tm * (unsigned)tn;
-    if (a.b_rows == 1)
-        product_kernel<T, 128, 128, 2, 2, true><<<grid, 256, 0, st>>>(a, tm, tn);
+    const auto tiles = [&](int64_t size) { return ((a.m + size - 1) / size) * ((a.n + size - 1) / size); };
+    if (a.m <= kFewRows)
+        few_rows<T, uint8_t>(a, st);
+    else if (sizeof(T) == 2 && tiles(256) >= 256)
+        product_tiles<T, 256, 256, 2, 4>(a, st);
+    else if (tiles(128) >= 256)
+        product_tiles<T, 128, 128, 2, 2>(a, st);
     else
-        product_kernel<T, 128, 128, 2, 2, false><<<grid, 256, 0, st>>>(a, tm, tn);
+        product_tiles<T, 64, 64, 2, 2>(a, st);
     return hipGetLastError();
 }
 
@@ -451,6 +591,17 @@ hipError_t launch_fp8_quantize(const QuantizeArgs& a, hipStream_t st) {
         case BCJR_TYPE_BF16: return quantize<__hip_bfloat16>(a, st);
         default: return quantize<_Float16>(a, st);
     }
+}
+
+bool fp8_few_rows(int64_t m) { return m <= kFewRows; }
+
+hipError_t launch_fp8_linear_few_rows(const ProductArgs& a, hipStream_t st) {
+    switch (a.out_type) {
+        case BCJR_TYPE_F32: few_rows<float, float>(a, st); break;
+        case BCJR_TYPE_BF16: few_rows<__hip_bfloat16, __hip_bfloat16>(a, st); break;
+        default: few_rows<_Float16, _Float16>(a, st); break;
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_fp8_product(const ProductArgs& a, hipStream_t st) {

@@ -26,6 +26,8 @@ bool dim(int64_t v) { return v >= 0 && v <= kMaxDim; }
 
 int64_t blocks(int64_t v, int64_t of) { return (v + of - 1) / of; }
 
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
 // An 8-bit matrix: 16-byte boundaries throughout, rows no closer than their length.
 bool rows16(const void* p, int64_t ld, int64_t cols) {
     return ((uintptr_t)p & 15u) == 0 && ld % 16 == 0 && ld >= cols && ld < kMaxTiles;
@@ -62,6 +64,40 @@ int fp8_block_matmul(const void* a, int64_t ld_a, const float* a_scale, const vo
     if (blocks(m, 16) * blocks(n, 16) > kMaxTiles) return BCJR_ERR_SIZE;
     const ProductArgs p{(const uint8_t*)a, a_scale, (const uint8_t*)b, b_scale, ld_a, ld_b, (int32_t)m, (int32_t)n,
                         (int32_t)k, b_block_rows, out, ld_out, out_type};
+    return hip_status(launch_fp8_product(p, (hipStream_t)stream));
+}
+
+size_t fp8_linear_quantized_workspace_bytes(int64_t m, int64_t k) {
+    if (!dim(m) || !dim(k) || m == 0 || k == 0 || fp8_few_rows(m)) return 0;
+    return align256((size_t)m * (size_t)blocks(k, 16) * 16) + (size_t)m * (size_t)blocks(k, 128) * sizeof(float);
+}
+
+int fp8_linear_quantized(const void* x, int32_t type, int64_t m, int64_t ld_x, const void* w, int64_t ld_w,
+                         const float* w_scale, int32_t w_block_rows, int64_t n, int64_t k, void* out, int64_t ld_out,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    if (!known_type(type) || (w_block_rows != 1 && w_block_rows != 128) || !dim(m) || !dim(n) || !dim(k))
+        return BCJR_ERR_SIZE;
+    if (m == 0 || n == 0) return BCJR_OK;
+    if (!out || (k > 0 && (!x || !w || !w_scale))) return BCJR_ERR_NULL;
+    if (ld_out < n || (k > 0 && (ld_x < k || !rows16(w, ld_w, k)))) return BCJR_ERR_LAYOUT;
+    if (blocks(m, 16) * blocks(n, 16) > kMaxTiles || blocks(m, 16) * blocks(k, 128) > kMaxTiles) return BCJR_ERR_SIZE;
+    const size_t need = fp8_linear_quantized_workspace_bytes(m, k);
+    if (need > 0 && (!workspace || ((uintptr_t)workspace & 255u) != 0 || workspace_bytes < need))
+        return BCJR_ERR_WORKSPACE;
+    ProductArgs p{(const uint8_t*)x, nullptr, (const uint8_t*)w, w_scale, ld_x, ld_w, (int32_t)m, (int32_t)n,
+                  (int32_t)k, w_block_rows, out, ld_out, type};
+    if (fp8_few_rows(m)) return hip_status(launch_fp8_linear_few_rows(p, (hipStream_t)stream));
+    if (need > 0) {
+        const int64_t ld = blocks(k, 16) * 16;
+        uint8_t* q = (uint8_t*)workspace;
+        float* scale = (float*)(q + align256((size_t)m * (size_t)ld));
+        const QuantizeArgs a{x, type, 1, m, k, ld_x, q, ld, scale, nullptr, 0, nullptr};
+        const hipError_t e = launch_fp8_quantize(a, (hipStream_t)stream);
+        if (e != hipSuccess) return BCJR_ERR_HIP;
+        p.a = q;
+        p.a_scale = scale;
+        p.ld_a = ld;
+    }
     return hip_status(launch_fp8_product(p, (hipStream_t)stream));
 }
 

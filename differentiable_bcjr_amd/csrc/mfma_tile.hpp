@@ -74,10 +74,11 @@ __device__ __forceinline__ void fetch_tail(const uint8_t* base, uint32_t ld, int
 }
 
 // Chunks g and g + 4 of row `row`.
-__device__ __forceinline__ void read_fragment(const uint8_t* lds, int row, int g, v4i& lo, v4i& hi) {
+__device__ __forceinline__ v8i read_slab(const uint8_t* lds, int row, int g) {
     const uint32_t pos = slab_chunk(row, g) * 16;
-    lo = *(const v4i*)(lds + row * kSlab + pos);
-    hi = *(const v4i*)(lds + row * kSlab + (pos ^ 64));
+    const v4i lo = *(const v4i*)(lds + row * kSlab + pos);
+    const v4i hi = *(const v4i*)(lds + row * kSlab + (pos ^ 64));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
 // Position of workgroup `id` of `count` in an order that gives each XCD one contiguous run of tiles, so that the

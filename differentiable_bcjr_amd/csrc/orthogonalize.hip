@@ -174,6 +174,16 @@ struct ProdArgs {
     int64_t out_batch;
 };
 
+// The first or second 32 halves of a slab.
+__device__ __forceinline__ v8h half_slab(v8i v, int h) {
+    return __builtin_bit_cast(v8h, h == 0 ? __builtin_shufflevector(v, v, 0, 1, 2, 3)
+                                          : __builtin_shufflevector(v, v, 4, 5, 6, 7));
+}
+
+__device__ __forceinline__ v4f multiply(v8h a, v8h b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
 template <Mode kMode, bool kSplit, class T, int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(ProdArgs a, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
@@ -225,20 +235,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(P
         if (s + 1 < slabs) fetch(s + 1, lds[(s + 1) & 1]);
         const uint8_t* lp = lds[s & 1];
         const uint8_t* lq = lp + BM * kSlab;
-        v4i fp[TM][2];
+        v8i fq[TN];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) read_fragment(lp, wm0 + i * 16 + r16, g, fp[i][0], fp[i][1]);
+        for (int j = 0; j < TN; ++j) fq[j] = read_slab(lq, wn0 + j * 16 + r16, g);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            v4i fq[2];
-            read_fragment(lq, wn0 + j * 16 + r16, g, fq[0], fq[1]);
+        for (int i = 0; i < TM; ++i) {
+            const v8i fp = read_slab(lp, wm0 + i * 16 + r16, g);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, fq[h]),
-                                                                       __builtin_bit_cast(v8h, fp[i][h]), acc[i][j], 0,
-                                                                       0, 0);
+                for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], h), half_slab(fp, h), acc[i][j]);
         }
     }
 
@@ -297,11 +303,26 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(P
     }
 }
 
+template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N>
+void launch_tiles(const ProdArgs& a, int64_t batch, hipStream_t st) {
+    const int tm = (a.rows + BM - 1) / BM, tn = (a.cols + BM - 1) / BM;
+    const unsigned tiles = kMode == kStep ? (unsigned)tm * tn : (unsigned)tm * (tm + 1) / 2;
+    ortho_product_kernel<kMode, kSplit, T, BM, BM, WAVES_M, WAVES_N>
+        <<<dim3(tiles, 1, (unsigned)batch), 64 * WAVES_M * WAVES_N, 0, st>>>(a, tm, tn);
+}
+
 template <Mode kMode, bool kSplit, class T>
 void launch_product(const ProdArgs& a, int64_t batch, hipStream_t st) {
-    const int tm = (a.rows + 127) / 128, tn = (a.cols + 127) / 128;
-    const unsigned tiles = kMode == kStep ? (unsigned)tm * tn : (unsigned)tm * (tm + 1) / 2;
-    ortho_product_kernel<kMode, kSplit, T, 128, 128, 2, 2><<<dim3(tiles, 1, (unsigned)batch), 256, 0, st>>>(a, tm, tn);
+    const auto tiles = [&](int64_t size) {
+        const int64_t tm = (a.rows + size - 1) / size, tn = (a.cols + size - 1) / size;
+        return batch * (kMode == kStep ? tm * tn : tm * (tm + 1) / 2);
+    };
+    if (tiles(256) >= 192)
+        launch_tiles<kMode, kSplit, T, 256, 2, 4>(a, batch, st);
+    else if (tiles(128) >= 192)
+        launch_tiles<kMode, kSplit, T, 128, 2, 2>(a, batch, st);
+    else
+        launch_tiles<kMode, kSplit, T, 64, 2, 2>(a, batch, st);
 }
 
 template <bool kSplit, class Out>

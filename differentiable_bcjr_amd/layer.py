@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import torch
 
-from . import BCJRError, _check, _nbytes, _ptr, _stream, abi   # noqa: F401  (BCJRError: what _check raises)
+from . import BCJRError, _check, _ptr, abi   # noqa: F401  (BCJRError: what _check raises)
 
 __all__ = ["fp8_block_quantize", "fp8_block_matmul", "fp8_linear", "fp8_linear_quantized", "orthogonalize"]
 
@@ -51,8 +51,20 @@ def _up(v: int, of: int) -> int:
     return -(-v // of)
 
 
+def _call(entry, device, *args) -> None:
+    """An entry point of the library on `device`'s current stream, with `device` current."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
+
+
 def _new_codes(rows: int, cols: int, device) -> torch.Tensor:
     """[rows, cols] codes whose rows start on 16-byte boundaries."""
+    if cols % 16 == 0:
+        return torch.empty((rows, cols), dtype=CODES, device=device)
     return torch.empty((rows, _up(cols, 16) * 16), dtype=CODES, device=device)[:, :cols]
 
 
@@ -68,10 +80,8 @@ def _quantize(x: torch.Tensor, block_rows: int, transposed: bool):
     q_t = s_t = None
     if transposed:
         q_t, s_t = _new_codes(cols, rows, dev), _new_scales(_up(cols, block_rows), _up(rows, BLOCK), dev)
-    with torch.cuda.device(dev):
-        _check(abi.fp8_block_quantize(x.data_ptr(), _TYPES[x.dtype], rows, cols, _row_distance(x), block_rows,
-                                      q.data_ptr(), _up(cols, 16) * 16, s.data_ptr(), _ptr(q_t),
-                                      _up(rows, 16) * 16, _ptr(s_t), _stream(dev)))
+    _call(abi.load().fp8_block_quantize, dev, x.data_ptr(), _TYPES[x.dtype], rows, cols, _row_distance(x), block_rows,
+          q.data_ptr(), _up(cols, 16) * 16, s.data_ptr(), _ptr(q_t), _up(rows, 16) * 16, _ptr(s_t))
     return (q, s, q_t, s_t) if transposed else (q, s)
 
 
@@ -108,9 +118,11 @@ def _scales(s, q: torch.Tensor, block_rows: int, name: str) -> torch.Tensor:
     shape = (_up(q.shape[0], block_rows), _up(q.shape[1], BLOCK))
     if not isinstance(s, torch.Tensor) or not s.is_cuda or s.dtype != torch.float32:
         raise TypeError(f"{name} must be a float32 CUDA (HIP) tensor")
-    if tuple(s.shape) != shape:
+    if s.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(s.shape)}")
-    return s if s.t().is_contiguous() else s.t().contiguous().t()
+    if (shape[0] == 1 or s.stride(0) == 1) and (shape[1] == 1 or s.stride(1) == shape[0]):
+        return s
+    return s.t().contiguous().t()
 
 
 def _weight_block(q, s, name: str) -> int:
@@ -120,18 +132,17 @@ def _weight_block(q, s, name: str) -> int:
     return BLOCK if s.shape[0] == _up(q.shape[0], BLOCK) else 1
 
 
-def _same_device(**tensors) -> None:
-    if len({t.device for t in tensors.values()}) != 1:
-        raise ValueError(f"{', '.join(tensors)} must be on one device")
+def _same_device(first, *others) -> None:
+    for t in others:
+        if t.device != first.device:
+            raise ValueError(f"tensors must be on one device, not {first.device} and {t.device}")
 
 
 def _matmul(a, a_scale, b, b_scale, b_rows: int, out_dtype) -> torch.Tensor:
     (m, k), n = a.shape, b.shape[0]
     out = torch.empty((m, n), dtype=out_dtype, device=a.device)
-    with torch.cuda.device(a.device):
-        _check(abi.fp8_block_matmul(a.data_ptr(), _code_distance(a), a_scale.data_ptr(), b.data_ptr(),
-                                    _code_distance(b), b_scale.data_ptr(), b_rows, m, n, k, out.data_ptr(),
-                                    _TYPES[out_dtype], max(n, 1), _stream(a.device)))
+    _call(abi.load().fp8_block_matmul, a.device, a.data_ptr(), _code_distance(a), a_scale.data_ptr(), b.data_ptr(),
+          _code_distance(b), b_scale.data_ptr(), b_rows, m, n, k, out.data_ptr(), _TYPES[out_dtype], max(n, 1))
     return out
 
 
@@ -145,7 +156,7 @@ def fp8_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_
     if a.shape[1] != b.shape[1]:
         raise ValueError(f"a and b must have rows of one length, not {a.shape[1]} and {b.shape[1]}")
     a_scale, b_scale = _scales(a_scale, a, 1, "a_scale"), _scales(b_scale, b, b_rows, "b_scale")
-    _same_device(a=a, a_scale=a_scale, b=b, b_scale=b_scale)
+    _same_device(a, a_scale, b, b_scale)
     return _matmul(a, a_scale, b, b_scale, b_rows, out_dtype)
 
 
@@ -154,7 +165,9 @@ def _tokens(x, k: int) -> torch.Tensor:
         raise TypeError("x must be a CUDA (HIP) tensor")
     if x.dim() < 1 or x.shape[-1] != k:
         raise ValueError(f"x must be [..., {k}], not {tuple(x.shape)}")
-    return _matrix(x.reshape(-1, k) if k else x.reshape(x.shape[:-1].numel(), 0), "x")
+    if x.dim() != 2:
+        x = x.reshape(x.shape[:-1].numel(), k)
+    return _matrix(x, "x")
 
 
 def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor) -> torch.Tensor:
@@ -162,10 +175,16 @@ def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor
     block_rows=128)``); x [..., K] is quantized on the way, a scale for each 128 of a row."""
     b_rows, w = _weight_block(w, w_scale, "w"), _codes(w, "w")
     w_scale = _scales(w_scale, w, b_rows, "w_scale")
-    rows = _tokens(x, w.shape[1])
-    _same_device(x=x, w=w, w_scale=w_scale)
-    y = _matmul(*_quantize(rows, 1, False), w, w_scale, b_rows, x.dtype)
-    return y.view(*x.shape[:-1], w.shape[0])
+    n, k = w.shape
+    rows = _tokens(x, k)
+    _same_device(x, w, w_scale)
+    m, dev, lib = rows.shape[0], x.device, abi.load()
+    y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=dev)
+    need = lib.fp8_linear_quantized_workspace_bytes(m, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call(lib.fp8_linear_quantized, dev, rows.data_ptr(), _TYPES[x.dtype], m, _row_distance(rows), w.data_ptr(),
+          _code_distance(w), w_scale.data_ptr(), b_rows, n, k, y.data_ptr(), max(n, 1), _ptr(ws), need)
+    return y
 
 
 class _Fp8Linear(torch.autograd.Function):
@@ -199,7 +218,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     128 x 128.  dx has x's type and dw has w's.  w may be the soft codeword (``soft_quantize``) of a layer's weights."""
     w = _matrix(w, "w")
     _tokens(x, w.shape[1])
-    _same_device(x=x, w=w)
+    _same_device(x, w)
     return _Fp8Linear.apply(x, w)
 
 
@@ -225,10 +244,9 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
             or g3.shape[0] > 1 and g3.stride(0) < 0):
         g3 = g3.contiguous()
     batch = g3.shape[0]
-    need = abi.orthogonalize_workspace_bytes(batch, rows, cols, out_type)
+    need = abi.load().orthogonalize_workspace_bytes(batch, rows, cols, out_type)
     ws = torch.empty(max(need, 1), dtype=torch.uint8, device=g.device)
-    with torch.cuda.device(g.device):
-        _check(abi.orthogonalize(g3.data_ptr(), in_type, batch, rows, cols, _row_distance(g3),
-                                 g3.stride(0) if batch > 1 else 0, int(steps), a, b, c, float(eps), out.data_ptr(),
-                                 out_type, ws.data_ptr(), _nbytes(ws), _stream(g.device)))
+    _call(abi.load().orthogonalize, g.device, g3.data_ptr(), in_type, batch, rows, cols, _row_distance(g3),
+          g3.stride(0) if batch > 1 else 0, int(steps), a, b, c, float(eps), out.data_ptr(), out_type, ws.data_ptr(),
+          need)
     return out
