@@ -39,6 +39,9 @@ BCJR_TYPE_F32 = 0
 BCJR_TYPE_BF16 = 1
 BCJR_TYPE_F16 = 2
 
+BCJR_GRAD_X = 1
+BCJR_GRAD_W = 2
+
 BCJR_NOALLOC_SCRATCH_BYTES = 256 << 20
 
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -73,6 +76,12 @@ _SIGNATURES = {
     "bcjr_soft_codeword_noalloc": ([_vp, _vp, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp], _int),
     "fp8_block_quantize": ([_vp, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp, _i64, _vp, _vp], _int),
     "fp8_block_matmul": ([_vp, _i64, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp], _int),
+    "fp8_linear_forward": ([_vp, _i32, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _sz, _vp, _sz,
+                            _vp], _int),
+    "fp8_linear_backward": ([_vp, _i32, _i64, _i64, _i64, _i64, _i32, _vp, _sz, _vp, _i64, _vp, _i32, _i64, _vp, _sz,
+                             _vp], _int),
+    "fp8_linear_saved_bytes": ([_i64, _i64, _i64, _i32], _sz),
+    "fp8_linear_workspace_bytes": ([_i64, _i64, _i64], _sz),
     "fp8_linear_quantized": ([_vp, _i32, _i64, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _vp, _i64, _vp, _sz, _vp], _int),
     "fp8_linear_quantized_workspace_bytes": ([_i64, _i64], _sz),
     "orthogonalize": ([_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _f32, _f32, _f32, _f32, _vp, _i32, _vp, _sz,

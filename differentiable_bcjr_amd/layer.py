@@ -187,28 +187,49 @@ def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor
     return y
 
 
+def _bytes(n: int, device) -> torch.Tensor | None:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _linear_forward(x, w, grads: int):
+    """(y, what the backward of `grads` needs): x [..., K] and w [N, K]."""
+    n, k = w.shape
+    rows = _tokens(x, k)
+    m, dev, lib = rows.shape[0], x.device, abi.load()
+    y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=dev)
+    keep, need = lib.fp8_linear_saved_bytes(m, n, k, grads), lib.fp8_linear_workspace_bytes(m, n, k)
+    saved, ws = _bytes(keep, dev), _bytes(need, dev)
+    _call(lib.fp8_linear_forward, dev, rows.data_ptr(), _TYPES[x.dtype], m, _row_distance(rows), w.data_ptr(),
+          _TYPES[w.dtype], n, _row_distance(w), k, grads, y.data_ptr(), max(n, 1), _ptr(saved), keep, _ptr(ws), need)
+    return y, saved
+
+
 class _Fp8Linear(torch.autograd.Function):
     """y = Q(x) Q(w)^T; dx = Q(dy) Q(w), dw = Q(dy^T) Q(x^T)^T.  Only codes and scales are kept for the backward."""
 
     @staticmethod
     def forward(ctx, x, w):
         need_x, need_w = ctx.needs_input_grad
-        xq = _quantize(_tokens(x, w.shape[1]), 1, need_w)
-        wq = _quantize(w, BLOCK, need_x)
-        ctx.save_for_backward(*(xq[2:] if need_w else (None, None)), *(wq[2:] if need_x else (None, None)))
-        ctx.like = x.shape, x.dtype, w.dtype
-        y = _matmul(*xq[:2], *wq[:2], BLOCK, x.dtype)
-        return y.view(*x.shape[:-1], w.shape[0])
+        grads = (abi.BCJR_GRAD_X if need_x else 0) | (abi.BCJR_GRAD_W if need_w else 0)
+        y, saved = _linear_forward(x, w, grads)
+        ctx.save_for_backward(saved)
+        ctx.like = x.shape, x.dtype, w.shape, w.dtype, grads
+        return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        need_x, need_w = ctx.needs_input_grad
-        xq_t, xs_t, wq_t, ws_t = ctx.saved_tensors
-        shape, x_type, w_type = ctx.like
-        dq = _quantize(_tokens(dy, dy.shape[-1]), 1, need_w)
-        dx = _matmul(*dq[:2], wq_t, ws_t, BLOCK, x_type).view(shape) if need_x else None
-        dw = _matmul(*dq[2:], xq_t, xs_t, 1, w_type) if need_w else None
+        (saved,) = ctx.saved_tensors
+        x_shape, x_type, (n, k), w_type, grads = ctx.like
+        rows, dev, lib = _tokens(dy, n), dy.device, abi.load()
+        m = rows.shape[0]
+        dx = torch.empty(x_shape, dtype=x_type, device=dev) if grads & abi.BCJR_GRAD_X else None
+        dw = torch.empty((n, k), dtype=w_type, device=dev) if grads & abi.BCJR_GRAD_W else None
+        need = lib.fp8_linear_workspace_bytes(m, n, k)
+        ws = _bytes(need, dev)
+        _call(lib.fp8_linear_backward, dev, rows.data_ptr(), _TYPES[x_type], m, _row_distance(rows), n, k, grads,
+              _ptr(saved), 0 if saved is None else saved.numel(), _ptr(dx), max(k, 1), _ptr(dw), _TYPES[w_type],
+              max(k, 1), _ptr(ws), need)
         return dx, dw
 
 
@@ -219,7 +240,9 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     w = _matrix(w, "w")
     _tokens(x, w.shape[1])
     _same_device(x, w)
-    return _Fp8Linear.apply(x, w)
+    if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
+        return _Fp8Linear.apply(x, w)
+    return _linear_forward(x, w, 0)[0]
 
 
 def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,

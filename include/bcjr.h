@@ -318,6 +318,26 @@ int fp8_block_matmul(const void* a, int64_t ld_a, const float* a_scale, const vo
                      int32_t out_type, int64_t ld_out, void* stream);
 
 /*
+ * The layer in training: out [m, n] = x w^T in x's type, and its gradients, every product in 8 bits:
+ *   out = Q(x) Q(w)^T,   dx = Q(dy) Q(w),   dw = Q(dy^T) Q(x^T)^T,
+ * Q with a scale for each 128 of a row along the sum (block_rows = 1), the weights with one for each 128 x 128.
+ * x [m, k], dy and dx are of `type`, w [n, k] of w_type, dw of dw_type.  `grads` says which gradients the backward will
+ * be asked for: the forward then leaves the codes of x^T and w^T that it needs in `saved`
+ * (fp8_linear_saved_bytes(m, n, k, grads) bytes), and the backward is called with the same sizes and grads.  Both use
+ * fp8_linear_workspace_bytes(m, n, k) bytes of workspace.  saved and workspace are 256-byte aligned
+ * (BCJR_ERR_WORKSPACE); where nothing is needed they may be NULL.
+ */
+enum { BCJR_GRAD_X = 1, BCJR_GRAD_W = 2 };
+int fp8_linear_forward(const void* x, int32_t type, int64_t m, int64_t ld_x, const void* w, int32_t w_type, int64_t n,
+                       int64_t ld_w, int64_t k, int32_t grads, void* out, int64_t ld_out, void* saved,
+                       size_t saved_bytes, void* workspace, size_t workspace_bytes, void* stream);
+int fp8_linear_backward(const void* dy, int32_t type, int64_t m, int64_t ld_dy, int64_t n, int64_t k, int32_t grads,
+                        const void* saved, size_t saved_bytes, void* dx, int64_t ld_dx, void* dw, int32_t dw_type,
+                        int64_t ld_dw, void* workspace, size_t workspace_bytes, void* stream);
+size_t fp8_linear_saved_bytes(int64_t m, int64_t n, int64_t k, int32_t grads);
+size_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
  * The layer of a served model: out [m, n] = x w^T in x's type, for weights w [n, k] quantized before (w_scale and
  * w_block_rows as b's above) and x [m, k] of `type`, quantized on the way as fp8_block_quantize does with
  * block_rows = 1.  The result is fp8_block_matmul's of those codes up to the order of its float32 sums.  Up to 16 rows

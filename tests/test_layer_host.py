@@ -19,6 +19,23 @@ def matmul(a=P, ld_a=16, a_s=P, b=P, ld_b=16, b_s=P, b_rows=1, m=8, n=8, k=8, ou
     return abi.fp8_block_matmul(a, ld_a, a_s, b, ld_b, b_s, b_rows, m, n, k, out, type, ld_out, None)
 
 
+def served(x=P, type=0, m=32, ld_x=16, w=P, ld_w=16, w_s=P, w_rows=128, n=8, k=16, out=P, ld_out=8, ws=P,
+           size=1 << 30):
+    return abi.fp8_linear_quantized(x, type, m, ld_x, w, ld_w, w_s, w_rows, n, k, out, ld_out, ws, size, None)
+
+
+def forward(x=P, type=0, m=8, ld_x=16, w=P, w_type=0, n=8, ld_w=16, k=16, grads=3, out=P, ld_out=8, saved=P,
+            keep=1 << 30, ws=P, size=1 << 30):
+    return abi.fp8_linear_forward(x, type, m, ld_x, w, w_type, n, ld_w, k, grads, out, ld_out, saved, keep, ws, size,
+                                  None)
+
+
+def backward(dy=P, type=0, m=8, ld_dy=8, n=8, k=16, grads=3, saved=P, keep=1 << 30, dx=P, ld_dx=16, dw=P, dw_type=0,
+             ld_dw=16, ws=P, size=1 << 30):
+    return abi.fp8_linear_backward(dy, type, m, ld_dy, n, k, grads, saved, keep, dx, ld_dx, dw, dw_type, ld_dw, ws,
+                                   size, None)
+
+
 def ortho(g=P, type=0, batch=1, rows=8, cols=8, ld=8, batch_g=64, steps=5, a=1.0, b=1.0, c=1.0, eps=0.0, out=P,
           out_type=0, ws=P, size=1 << 40):
     return abi.orthogonalize(g, type, batch, rows, cols, ld, batch_g, steps, a, b, c, eps, out, out_type, ws, size, None)
@@ -46,6 +63,51 @@ def test_quantize_refusals(change, status):
     (dict(m=1 << 30, n=1 << 30, ld_out=1 << 30), abi.BCJR_ERR_SIZE), (dict(m=0), abi.BCJR_OK), (dict(n=0), abi.BCJR_OK)])
 def test_matmul_refusals(change, status):
     assert matmul(**change) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(x=None), abi.BCJR_ERR_NULL), (dict(w=None), abi.BCJR_ERR_NULL), (dict(w_s=None), abi.BCJR_ERR_NULL),
+    (dict(out=None), abi.BCJR_ERR_NULL), (dict(type=7), abi.BCJR_ERR_SIZE), (dict(w_rows=16), abi.BCJR_ERR_SIZE),
+    (dict(m=-1), abi.BCJR_ERR_SIZE), (dict(ld_x=15), abi.BCJR_ERR_LAYOUT), (dict(w=P + 2), abi.BCJR_ERR_LAYOUT),
+    (dict(ld_w=17), abi.BCJR_ERR_LAYOUT), (dict(ld_out=7), abi.BCJR_ERR_LAYOUT), (dict(ws=None), abi.BCJR_ERR_WORKSPACE),
+    (dict(ws=P + 16), abi.BCJR_ERR_WORKSPACE), (dict(size=100), abi.BCJR_ERR_WORKSPACE), (dict(m=0), abi.BCJR_OK),
+    (dict(n=0), abi.BCJR_OK)])
+def test_linear_quantized_refusals(change, status):
+    assert served(**change) == status
+
+
+@pytest.mark.parametrize("call,change,status", [
+    (forward, dict(x=None), abi.BCJR_ERR_NULL), (forward, dict(w=None), abi.BCJR_ERR_NULL),
+    (forward, dict(out=None), abi.BCJR_ERR_NULL), (forward, dict(type=4), abi.BCJR_ERR_SIZE),
+    (forward, dict(w_type=4), abi.BCJR_ERR_SIZE), (forward, dict(grads=4), abi.BCJR_ERR_SIZE),
+    (forward, dict(k=BIG), abi.BCJR_ERR_SIZE), (forward, dict(ld_x=8), abi.BCJR_ERR_LAYOUT),
+    (forward, dict(ld_w=8), abi.BCJR_ERR_LAYOUT), (forward, dict(ld_out=7), abi.BCJR_ERR_LAYOUT),
+    (forward, dict(saved=None), abi.BCJR_ERR_WORKSPACE), (forward, dict(keep=16), abi.BCJR_ERR_WORKSPACE),
+    (forward, dict(saved=P + 16), abi.BCJR_ERR_WORKSPACE), (forward, dict(ws=None), abi.BCJR_ERR_WORKSPACE),
+    (forward, dict(size=16), abi.BCJR_ERR_WORKSPACE), (backward, dict(dy=None), abi.BCJR_ERR_NULL),
+    (backward, dict(dx=None), abi.BCJR_ERR_NULL), (backward, dict(dw=None), abi.BCJR_ERR_NULL),
+    (backward, dict(type=-1), abi.BCJR_ERR_SIZE), (backward, dict(dw_type=5), abi.BCJR_ERR_SIZE),
+    (backward, dict(grads=-1), abi.BCJR_ERR_SIZE), (backward, dict(ld_dy=7), abi.BCJR_ERR_LAYOUT),
+    (backward, dict(ld_dx=15), abi.BCJR_ERR_LAYOUT), (backward, dict(ld_dw=15), abi.BCJR_ERR_LAYOUT),
+    (backward, dict(keep=16), abi.BCJR_ERR_WORKSPACE), (backward, dict(ws=P + 64), abi.BCJR_ERR_WORKSPACE),
+    (backward, dict(size=16), abi.BCJR_ERR_WORKSPACE)])
+def test_linear_refusals(call, change, status):
+    assert call(**change) == status
+
+
+def test_linear_buffers():
+    saved, ws = abi.fp8_linear_saved_bytes, abi.fp8_linear_workspace_bytes
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    m, n, k = 100, 60, 40
+    # x^T [k, m] with a scale for each row and 128 of m, w^T [k, n] with one for each 128 x 128; rows on 16 bytes
+    x_t, w_t = up(k * 112) + up(k * 4), up(k * 64) + up(4)
+    assert [saved(m, n, k, g) for g in range(4)] == [0, w_t, x_t, x_t + w_t]
+    forward_ws = up(m * 48) + up(m * 4) + up(n * 48) + up(4)
+    backward_ws = up(m * 64) + up(m * 4) + up(n * 112) + up(n * 4)
+    assert ws(m, n, k) == max(forward_ws, backward_ws)
+    assert abi.fp8_linear_quantized_workspace_bytes(16, k) == 0
+    assert abi.fp8_linear_quantized_workspace_bytes(m, k) == up(m * 48) + up(m * 4)
+    assert saved(-1, n, k, 3) == ws(m, BIG, k) == abi.fp8_linear_quantized_workspace_bytes(-1, k) == 0
 
 
 @pytest.mark.parametrize("change,status", [
