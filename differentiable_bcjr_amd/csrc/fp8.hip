@@ -304,6 +304,7 @@ template <class T, int BM, int BN, int WAVES_M, int WAVES_N, bool kRowScales>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(ProductArgs a, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
     constexpr bool kWide = sizeof(T) == 4;
+    constexpr bool kPaced = !kWide && !kRowScales;   // the order of MFMAs and multiply-adds is prescribed
     constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
     static_assert(kRowScales || 128 % (BN / WAVES_N) == 0, "a wave's columns lie in one block of b");
     __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kSlab];
@@ -316,24 +317,15 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
     const uint8_t* pa = a.a + (int64_t)m0 * a.ld_a;
     const uint8_t* pb = a.b + (int64_t)n0 * a.ld_b;
     const int rows_a = a.m - m0, rows_b = a.n - n0;
-    const int slabs = (a.k + kSlab - 1) / kSlab;
     const int r16 = lane & 15, g = lane >> 4;
 
-    auto fetch = [&](int s, uint8_t* to) {
-        const int left = a.k - s * kSlab;
-        if (left >= kSlab) {
-            fetch_slab<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, s * kSlab, to, wave, lane);
-            fetch_slab<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, s * kSlab, to + BM * kSlab, wave, lane);
-        } else {
-            fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, s * kSlab, left, to, wave, lane);
-            fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, s * kSlab, left, to + BM * kSlab, wave, lane);
-        }
-    };
+    SlabSource<BM, kWaves> src_a;
+    SlabSource<BN, kWaves> src_b;
+    src_a.set(pa, (uint32_t)a.ld_a, rows_a, wave, lane);
+    src_b.set(pb, (uint32_t)a.ld_b, rows_b, wave, lane);
 
     const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
-    int ma[TM];   // rows of a whose scales this lane applies
-#pragma unroll
-    for (int i = 0; i < TM; ++i) ma[i] = min(m0 + wm0 + i * 16 + r16, a.m - 1);
+    const int m_first = m0 + wm0 + r16;   // rows of a whose scales this lane applies: m_first + 16 i
     const int sb_len = kRowScales ? a.n : (a.n + 127) / 128;
     const int sb_at = kRowScales ? 0 : min((n0 + wn0) / 128, sb_len - 1);
 
@@ -345,28 +337,27 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
 
     // The scales of a slab are loaded ahead of the next slab's operands, a step before their use: loads complete in
     // order, so a load behind the operands would be waited for with them.
-    float sa_next[TM], sb_next[TN][4];
+    float sa_next[TM], sb_next[kRowScales ? TN : 1][4];
     auto fetch_scales = [&](int s) {
+        const float* pa_s = a.a_scale + (int64_t)s * a.m;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa_next[i] = a.a_scale[(int64_t)s * a.m + ma[i]];
+        for (int i = 0; i < TM; ++i) sa_next[i] = pa_s[min(m_first + i * 16, a.m - 1)];
         if constexpr (kRowScales) {
+            const float* pb_s = a.b_scale + (int64_t)s * a.n;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    sb_next[j][e] = a.b_scale[(int64_t)s * a.n + min(n0 + wn0 + j * 16 + g * 4 + e, a.n - 1)];
+                for (int e = 0; e < 4; ++e) sb_next[j][e] = pb_s[min(n0 + wn0 + j * 16 + g * 4 + e, a.n - 1)];
         } else {
             sb_next[0][0] = a.b_scale[(int64_t)s * sb_len + sb_at];
         }
     };
-    if (slabs > 0) {
-        fetch_scales(0);
-        fetch(0, lds[0]);
-    }
-    for (int s = 0; s < slabs; ++s) {
-        wait_loads();
-        __syncthreads();   // slab s is in LDS, and nobody reads the other buffer any more
-        float sa[TM], sb[TN][4];
+
+    // One slab: the fragments of b stay in registers, those of a pass through one ahead of their use, and a row of
+    // tiles' sums are scaled and added while the next row's MFMAs run (a lone MFMA followed by the use of its result
+    // would leave the matrix core idle for its latency).
+    float sa[TM], sb[kRowScales ? TN : 1][4];
+    auto take_scales = [&] {
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = kRowScales ? sa_next[i] : sa_next[i] * sb_next[0][0];
         if constexpr (kRowScales) {
@@ -375,55 +366,96 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sb[j][e] = sb_next[j][e];
         }
-        if (s + 1 < slabs) {
-            fetch_scales(s + 1);
-            fetch(s + 1, lds[(s + 1) & 1]);
-        }
-        const uint8_t* la = lds[s & 1];
+    };
+    auto multiply = [&](const uint8_t* la) {
         const uint8_t* lb = la + BM * kSlab;
         Fragment<kWide> fb[TN];
+        v8i fa[2];
 #pragma unroll
         for (int j = 0; j < TN; ++j) fb[j].set(read_slab(lb, wn0 + j * 16 + r16, g));
+        fa[0] = read_slab(la, wm0 + r16, g);
+        v4f p[2][TN];
+        if constexpr (kPaced) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            Fragment<kWide> fa;
-            fa.set(read_slab(la, wm0 + i * 16 + r16, g));
+        for (int i = 0; i <= TM; ++i) {
+            if (i + 1 < TM) fa[(i + 1) & 1] = read_slab(la, wm0 + (i + 1) * 16 + r16, g);
+            if (i < TM) {
+                Fragment<kWide> f;
+                f.set(fa[i & 1]);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const v4f p = block_product(fb[j].v, fa.v);
+                for (int j = 0; j < TN; ++j) p[i & 1][j] = block_product(fb[j].v, f.v);
+            }
+            if (i > 0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (kRowScales)
-                        acc[i][j][e] = fmaf(p[e] * sb[j][e], sa[i], acc[i][j][e]);
-                    else
-                        acc[i][j][e] = fmaf(p[e], sa[i], acc[i][j][e]);
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = p[(i - 1) & 1][j][e];
+                        if constexpr (kRowScales)
+                            acc[i - 1][j][e] = fmaf(v * sb[j][e], sa[i - 1], acc[i - 1][j][e]);
+                        else
+                            acc[i - 1][j][e] = fmaf(v, sa[i - 1], acc[i - 1][j][e]);
+                    }
+            }
+            if constexpr (kPaced) {
+                if (i + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // the next fragment of a
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    if (i < TM) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // one MFMA
+                    if (i > 0) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);      // four multiply-adds
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+    };
+
+    const int full = a.k / kSlab, tail = a.k % kSlab;
+    if (full > 0) {
+        fetch_scales(0);
+        src_a.fetch(0, lds[0], wave);
+        src_b.fetch(0, lds[0] + BM * kSlab, wave);
+    }
+    for (int s = 0; s < full; ++s) {
+        wait_loads();
+        __syncthreads();   // slab s is in LDS, and nobody reads the other buffer any more
+        const uint8_t* now = lds[s & 1];
+        take_scales();
+        if (s + 1 < full) {
+            fetch_scales(s + 1);
+            uint8_t* next = lds[(s + 1) & 1];
+            src_a.fetch((uint32_t)(s + 1) * kSlab, next, wave);
+            src_b.fetch((uint32_t)(s + 1) * kSlab, next + BM * kSlab, wave);
+        }
+        multiply(now);
+    }
+    if (tail) {
+        __syncthreads();
+        fetch_scales(full);
+        fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, (uint32_t)full * kSlab, tail, lds[0], wave, lane);
+        fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, (uint32_t)full * kSlab, tail, lds[0] + BM * kSlab, wave,
+                               lane);
+        __syncthreads();
+        take_scales();
+        multiply(lds[0]);
     }
 
-    T* out = (T*)a.out;
-    const bool wide = ((uintptr_t)out % (4 * sizeof(T)) == 0) && (a.ld_out % 4 == 0);
+    using Tile = WaveTile<T, TM * 16, TN * 16>;
+    static_assert(kWaves * Tile::kBytes <= (int)sizeof(lds), "every wave's results fit in LDS");
+    __syncthreads();   // nobody reads the operands any more
+    uint8_t* mine = lds[0] + wave * Tile::kBytes;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int m = m0 + wm0 + i * 16 + r16;
-        if (m >= a.m) continue;
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int n = n0 + wn0 + j * 16 + g * 4;
             T e[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) e[x] = from_f32<T>(acc[i][j][x]);
-            T* to = out + (int64_t)m * a.ld_out + n;
-            if (wide && n + 4 <= a.n) {
-                __builtin_memcpy(__builtin_assume_aligned(to, 4 * sizeof(T)), e, sizeof(e));
-            } else {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    if (n + x < a.n) to[x] = e[x];
-            }
+            Tile::put(mine, i * 16 + r16, j * 16 + g * 4, e);
         }
-    }
+    wave_fence();
+    const bool wide = (uintptr_t)a.out % 16 == 0 && (a.ld_out * sizeof(T)) % 16 == 0;
+    Tile::store(mine, (T*)a.out + (int64_t)(m0 + wm0) * a.ld_out + n0 + wn0, a.ld_out, rows_a - wm0, rows_b - wn0, wide,
+                lane);
 }
 
 // ---- few rows
@@ -572,11 +604,17 @@ void product_tiles(const ProductArgs& a, hipStream_t st) {
 template <class T>
 hipError_t product(const ProductArgs& a, hipStream_t st) {
     const auto tiles = [&](int64_t size) { return ((a.m + size - 1) / size) * ((a.n + size - 1) / size); };
-    if (a.m <= kFewRows)
+    if (a.m <= kFewRows) {
         few_rows<T, uint8_t>(a, st);
-    else if (sizeof(T) == 2 && tiles(256) >= 256)
-        product_tiles<T, 256, 256, 2, 4>(a, st);
-    else if (tiles(128) >= 256)
+        return hipGetLastError();
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (tiles(256) >= 256) {
+            product_tiles<T, 256, 256, 2, 4>(a, st);
+            return hipGetLastError();
+        }
+    }
+    if (tiles(128) >= 256)
         product_tiles<T, 128, 128, 2, 2>(a, st);
     else
         product_tiles<T, 64, 64, 2, 2>(a, st);

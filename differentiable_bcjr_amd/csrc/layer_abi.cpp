@@ -12,7 +12,8 @@ namespace {
 
 using namespace bcjr;
 
-constexpr int64_t kMaxDim = (int64_t)1 << 30;       // rows, columns and reduction lengths of the 8-bit operators
+constexpr int64_t kMaxDim = (int64_t)1 << 23;       // rows, columns and reduction lengths of the 8-bit operators
+constexpr int64_t kMaxDistance = (int64_t)1 << 23;  // bytes between the rows of 8-bit operands: a tile's 256 rows within 2^31
 constexpr int64_t kMaxTiles = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxUpdateDim = 65536;
 constexpr int64_t kMaxBatch = 65535;                // a grid's third dimension
@@ -30,7 +31,7 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // An 8-bit matrix: 16-byte boundaries throughout, rows no closer than their length.
 bool rows16(const void* p, int64_t ld, int64_t cols) {
-    return ((uintptr_t)p & 15u) == 0 && ld % 16 == 0 && ld >= cols && ld < kMaxTiles;
+    return ((uintptr_t)p & 15u) == 0 && ld % 16 == 0 && ld >= cols && ld <= kMaxDistance;
 }
 
 // Room for the codes and scales of a matrix in a caller's buffer, each part on a 256-byte boundary.

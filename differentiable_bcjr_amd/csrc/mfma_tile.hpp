@@ -35,20 +35,35 @@ __device__ __forceinline__ void load_to_lds(const void* g, void* lds) {
 // Every load this wave has issued is complete (those to LDS too, which a barrier alone does not wait for).
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// ROWS rows of one slab into LDS by NW waves; rows from `rows` on repeat the last one (their results are not stored).
+// ROWS rows of an operand, of which NW waves fetch one slab after the other: lane l of a wave's i-th instruction brings
+// 16 bytes of row 8 (i NW + wave) + l / 8.  Rows from `rows` on repeat the last one (their results are not stored).  The
+// lanes' offsets stay in registers; what changes from slab to slab is the uniform base.
 template <int ROWS, int NW>
-__device__ __forceinline__ void fetch_slab(const uint8_t* base, uint32_t ld, int rows, uint32_t kbyte, uint8_t* lds,
-                                           int wave, int lane) {
+struct SlabSource {
     static_assert(ROWS % (8 * NW) == 0, "whole instructions for every wave");
+    static constexpr int kLoads = ROWS / (8 * NW);
+    const uint8_t* base;
+    uint32_t offset[kLoads];
+
+    __device__ __forceinline__ void set(const uint8_t* first_row, uint32_t ld, int rows, int wave, int lane) {
+        base = first_row;
 #pragma unroll
-    for (int i = 0; i < ROWS / (8 * NW); ++i) {
-        const int part = i * NW + wave;
-        const int row = part * 8 + (lane >> 3);
-        const int r = row < rows ? row : rows - 1;
-        load_to_lds(base + ((size_t)((uint32_t)r * (uint64_t)ld) + kbyte + slab_chunk(row, lane & 7) * 16),
-                    lds + part * 1024);
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = (i * NW + wave) * 8 + (lane >> 3);
+            offset[i] = (uint32_t)min(row, rows - 1) * ld + slab_chunk(row, lane & 7) * 16;
+        }
     }
-}
+
+    __device__ __forceinline__ void fetch(uint32_t kbyte, uint8_t* lds, int wave) const {
+        const uint8_t* from = base + kbyte;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t at = offset[i];
+            asm("" : "+v"(at));   // widened here and not ahead of the loop: a register, not two, and a scalar base
+            load_to_lds(from + at, lds + (i * NW + wave) * 1024);
+        }
+    }
+};
 
 // The last slab of a row length that is no multiple of 128: `valid` bytes are there, the rest is written as zeros.
 template <int ROWS, int NW>
@@ -80,6 +95,62 @@ __device__ __forceinline__ v8i read_slab(const uint8_t* lds, int row, int g) {
     const v4i hi = *(const v4i*)(lds + row * kSlab + (pos ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
+
+// What this wave wrote to LDS is there for its other lanes.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// A wave's tile of ROWS x COLS results on their way to memory: each lane of an MFMA holds four neighbours of one row, so
+// stored directly the 16 rows of an instruction get 32 bytes each.  They pass through LDS instead and leave as whole
+// rows of the tile.  LDS holds 16-byte chunks, permuted within a row so that neither side's accesses collide: rows r and
+// r + R share banks (R = 256 bytes / row), so the permutation changes every R rows.
+template <class T, int ROWS, int COLS>
+struct WaveTile {
+    static constexpr int kRowBytes = COLS * (int)sizeof(T);
+    static constexpr int kChunks = kRowBytes / 16;
+    static constexpr int kBytes = ROWS * kRowBytes;
+    static constexpr int kPeriod = kRowBytes >= 256 ? 1 : 256 / kRowBytes;
+    static constexpr int kPer = 16 / (int)sizeof(T);   // elements of a chunk
+    static_assert((kChunks & (kChunks - 1)) == 0 && kChunks <= 64, "");
+
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) {
+        return (uint32_t)(row * kRowBytes + (chunk ^ ((row / kPeriod) & (kChunks - 1))) * 16);
+    }
+    // v[0..3] at row `row`, columns col .. col + 3 (col a multiple of 4)
+    static __device__ __forceinline__ void put(uint8_t* lds, int row, int col, const T (&v)[4]) {
+        __builtin_memcpy(__builtin_assume_aligned(lds + at(row, col / kPer) + (col % kPer) * sizeof(T), 4 * sizeof(T)),
+                         v, sizeof(v));
+    }
+    // element at (row, col)
+    static __device__ __forceinline__ void put1(uint8_t* lds, int row, int col, T v) {
+        *(T*)(lds + at(row, col / kPer) + (col % kPer) * sizeof(T)) = v;
+    }
+    // The tile's rows to out (its first element's place; ld elements a row), the first `rows` rows and `cols` columns of
+    // it.  `wide`: out and ld are on 16-byte boundaries.
+    static __device__ __forceinline__ void store(const uint8_t* lds, T* out, int64_t ld, int rows, int cols, bool wide,
+                                                 int lane) {
+        constexpr int kRowsPer = 64 / kChunks;   // rows of one instruction
+#pragma unroll 4
+        for (int i = 0; i < ROWS / kRowsPer; ++i) {
+            const int row = i * kRowsPer + lane / kChunks, chunk = lane % kChunks;
+            const v4i w = *(const v4i*)(lds + at(row, chunk));
+            const int left = cols - chunk * kPer;
+            if (row >= rows || left <= 0) continue;
+            T* to = out + (int64_t)row * ld + chunk * kPer;
+            if (wide && left >= kPer) {
+                *(v4i*)to = w;
+            } else {
+                T e[kPer];
+                __builtin_memcpy(e, &w, 16);
+#pragma unroll
+                for (int x = 0; x < kPer; ++x)
+                    if (x < left) to[x] = e[x];
+            }
+        }
+    }
+};
 
 // Position of workgroup `id` of `count` in an order that gives each XCD one contiguous run of tiles, so that the
 // workgroups that share an L2 share operand rows.

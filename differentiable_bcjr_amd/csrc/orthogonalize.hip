@@ -214,11 +214,17 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(P
     const uint8_t* p_lo = kSplit ? (const uint8_t*)(a.p_lo + item * a.p_batch + (int64_t)m0 * a.k) : nullptr;
     const uint8_t* q_lo = kSplit ? (const uint8_t*)(a.q_lo + item * a.q_batch + (int64_t)n0 * a.k) : nullptr;
 
+    SlabSource<BM, kWaves> src_p;
+    SlabSource<BN, kWaves> src_q;
+    src_p.set(p_hi, ld, a.rows - m0, wave, lane);
+    src_q.set(q_hi, ld, a.cols - n0, wave, lane);
     auto fetch = [&](int s, uint8_t* to) {
         const int part = kSplit ? s / per : 0;   // hi hi, hi lo, lo hi
         const uint32_t at = (uint32_t)(s - part * per) * kSlab;
-        fetch_slab<BM, kWaves>(kSplit && part == 2 ? p_lo : p_hi, ld, a.rows - m0, at, to, wave, lane);
-        fetch_slab<BN, kWaves>(kSplit && part == 1 ? q_lo : q_hi, ld, a.cols - n0, at, to + BM * kSlab, wave, lane);
+        src_p.base = kSplit && part == 2 ? p_lo : p_hi;
+        src_q.base = kSplit && part == 1 ? q_lo : q_hi;
+        src_p.fetch(at, to, wave);
+        src_q.fetch(at, to + BM * kSlab, wave);
     };
 
     v4f acc[TM][TN];

@@ -280,7 +280,7 @@ int bcjr_soft_codeword_noalloc(const float* w, const float* codebook, int64_t B,
  * layer, and turn the gradient of the weights into an update.  As above, every tensor pointer is a device pointer owned
  * by the caller, nothing is allocated or synchronized, and every check but BCJR_ERR_HIP runs before any launch.  Row
  * distances (ld_*) are in elements of the array.  Matrices with no rows or no columns are accepted and leave their
- * outputs untouched (a product over k = 0 writes zeros).  Row counts, column counts and k are at most 2^30.
+ * outputs untouched (a product over k = 0 writes zeros).  Row counts, column counts and k are at most 2^23.
  */
 enum { BCJR_TYPE_F32 = 0, BCJR_TYPE_BF16 = 1, BCJR_TYPE_F16 = 2 };
 
@@ -311,7 +311,7 @@ int fp8_block_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, 
  * For a bfloat16 or float16 result the 8-bit matrix instruction sums it, which cuts the products of 8 neighbouring k
  * 13 bits below the largest exponent among them (a relative error near 1e-4 on random data, under the result's own
  * rounding).  a and b lie on 16-byte boundaries with ld_a, ld_b multiples of 16
- * below 2^31 (BCJR_ERR_LAYOUT); bytes behind a row's k codes are not used.
+ * up to 2^23 (BCJR_ERR_LAYOUT); bytes behind a row's k codes are not used.
  */
 int fp8_block_matmul(const void* a, int64_t ld_a, const float* a_scale, const void* b, int64_t ld_b,
                      const float* b_scale, int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* out,
