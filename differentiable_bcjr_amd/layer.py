@@ -25,64 +25,67 @@ CODES = torch.float8_e4m3fn
 _TYPES = {torch.float32: abi.BCJR_TYPE_F32, torch.bfloat16: abi.BCJR_TYPE_BF16, torch.float16: abi.BCJR_TYPE_F16}
 
 
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_lib = None
+
+
+def _entry():
+    global _lib
+    if _lib is None:
+        _lib = abi.load()
+    return _lib
+
+
+def _call(entry, index: int, *args) -> None:
+    """An entry point of the library on device `index`'s current stream, with that device current."""
+    if index == _device():
+        status = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, _raw_stream(index))
+    if status:
+        _check(status)
+
+
 def _type(dtype, name: str) -> int:
     if dtype not in _TYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, not {dtype}")
     return _TYPES[dtype]
 
 
-def _matrix(x, name: str) -> torch.Tensor:
-    """A float matrix whose rows lie one after the other (any distance apart); copied where they do not."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    _type(x.dtype, name)
-    if x.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
-        x = x.contiguous()
-    return x
-
-
-def _row_distance(x: torch.Tensor) -> int:
-    return x.stride(-2) if x.shape[-2] > 1 else max(x.shape[-1], 1)
-
-
 def _up(v: int, of: int) -> int:
     return -(-v // of)
 
 
-def _call(entry, device, *args) -> None:
-    """An entry point of the library on `device`'s current stream, with `device` current."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
-    else:
-        with torch.cuda.device(device):
-            _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
+def _matrix(x, name: str):
+    """(x, type, rows, columns, distance of rows) of a float matrix whose rows lie one after the other, any distance
+    apart; a copy where they do not."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    t = _TYPES.get(x.dtype)
+    if t is None:
+        _type(x.dtype, name)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    (rows, cols), (ld, step) = x.shape, x.stride()
+    if rows <= 1:
+        ld = max(cols, 1)
+    if cols > 1 and step != 1 or ld < cols:
+        x, ld = x.contiguous(), max(cols, 1)
+    return x, t, rows, cols, ld
 
 
-def _new_codes(rows: int, cols: int, device) -> torch.Tensor:
-    """[rows, cols] codes whose rows start on 16-byte boundaries."""
-    if cols % 16 == 0:
-        return torch.empty((rows, cols), dtype=CODES, device=device)
-    return torch.empty((rows, _up(cols, 16) * 16), dtype=CODES, device=device)[:, :cols]
+def _new_codes(rows: int, cols: int, device):
+    """[rows, cols] codes whose rows start on 16-byte boundaries, and their distance."""
+    ld = (cols + 15) // 16 * 16 or 16
+    return torch.empty_strided((rows, cols), (ld, 1), dtype=CODES, device=device), ld
 
 
-def _new_scales(row_blocks: int, col_blocks: int, device) -> torch.Tensor:
-    """[row_blocks, col_blocks] scales that lie column by column: a step of a product reads one column."""
-    return torch.empty((col_blocks, row_blocks), dtype=torch.float32, device=device).t()
-
-
-def _quantize(x: torch.Tensor, block_rows: int, transposed: bool):
-    rows, cols = x.shape
-    dev = x.device
-    q, s = _new_codes(rows, cols, dev), _new_scales(_up(rows, block_rows), _up(cols, BLOCK), dev)
-    q_t = s_t = None
-    if transposed:
-        q_t, s_t = _new_codes(cols, rows, dev), _new_scales(_up(cols, block_rows), _up(rows, BLOCK), dev)
-    _call(abi.load().fp8_block_quantize, dev, x.data_ptr(), _TYPES[x.dtype], rows, cols, _row_distance(x), block_rows,
-          q.data_ptr(), _up(cols, 16) * 16, s.data_ptr(), _ptr(q_t), _up(rows, 16) * 16, _ptr(s_t))
-    return (q, s, q_t, s_t) if transposed else (q, s)
+def _new_scales(rows: int, cols: int, block_rows: int, device) -> torch.Tensor:
+    """Scales of a matrix, column by column: a step of a product reads one column."""
+    blocks = rows if block_rows == 1 else _up(rows, block_rows)
+    return torch.empty_strided((blocks, (cols + 127) // 128), (1, blocks or 1), dtype=torch.float32, device=device)
 
 
 def fp8_block_quantize(x: torch.Tensor, *, block_rows: int = 1, transposed: bool = False):
@@ -91,99 +94,108 @@ def fp8_block_quantize(x: torch.Tensor, *, block_rows: int = 1, transposed: bool
     and gradients) or of 128 rows (``block_rows=128``, weights).  q scale stands for x, with scale = amax / 448 (at
     least 2^-126).  With ``transposed`` also (q_t [K, M], scale_t [ceil(K / block_rows), ceil(M / 128)]) of the
     transpose, from the same pass over x.  An Inf or NaN makes the values of its block NaN."""
-    x = _matrix(x, "x")
+    x, x_type, rows, cols, ld = _matrix(x, "x")
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    return _quantize(x, block_rows, transposed)
+    dev = x.device
+    q, ld_q = _new_codes(rows, cols, dev)
+    s = _new_scales(rows, cols, block_rows, dev)
+    if not transposed:
+        _call(_entry().fp8_block_quantize, dev.index, x.data_ptr(), x_type, rows, cols, ld, block_rows, q.data_ptr(),
+              ld_q, s.data_ptr(), None, 0, None)
+        return q, s
+    q_t, ld_qt = _new_codes(cols, rows, dev)
+    s_t = _new_scales(cols, rows, block_rows, dev)
+    _call(_entry().fp8_block_quantize, dev.index, x.data_ptr(), x_type, rows, cols, ld, block_rows, q.data_ptr(), ld_q,
+          s.data_ptr(), q_t.data_ptr(), ld_qt, s_t.data_ptr())
+    return q, s, q_t, s_t
 
 
-def _codes(q, name: str) -> torch.Tensor:
-    """Codes whose rows lie on 16-byte boundaries; copied where they do not."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype != CODES:
+def _codes(q, name: str):
+    """(q, rows, columns, distance of rows) of a matrix of codes whose rows lie on 16-byte boundaries; a copy where
+    they do not."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dtype is not CODES:
         raise TypeError(f"{name} must be a float8_e4m3fn CUDA (HIP) tensor")
     if q.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
-    rows, cols = q.shape
-    if (cols > 1 and q.stride(1) != 1 or q.data_ptr() % 16
-            or rows > 1 and (q.stride(0) % 16 or q.stride(0) < cols)):
-        q = _new_codes(rows, cols, q.device).copy_(q)
-    return q
+    (rows, cols), (ld, step) = q.shape, q.stride()
+    if rows <= 1:
+        ld = (cols + 15) // 16 * 16 or 16
+    if cols > 1 and step != 1 or ld % 16 or ld < cols or q.data_ptr() % 16:
+        packed, ld = _new_codes(rows, cols, q.device)
+        q = packed.copy_(q)
+    return q, rows, cols, ld
 
 
-def _code_distance(q: torch.Tensor) -> int:
-    return q.stride(0) if q.shape[0] > 1 else _up(max(q.shape[1], 1), 16) * 16
-
-
-def _scales(s, q: torch.Tensor, block_rows: int, name: str) -> torch.Tensor:
-    shape = (_up(q.shape[0], block_rows), _up(q.shape[1], BLOCK))
-    if not isinstance(s, torch.Tensor) or not s.is_cuda or s.dtype != torch.float32:
+def _scales(s, row_blocks: int, col_blocks: int, like: torch.Tensor, name: str) -> torch.Tensor:
+    """The scales of a matrix on `like`'s device, column by column; a copy where they lie otherwise."""
+    if not isinstance(s, torch.Tensor) or s.dtype is not torch.float32:
         raise TypeError(f"{name} must be a float32 CUDA (HIP) tensor")
-    if s.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(s.shape)}")
-    if (shape[0] == 1 or s.stride(0) == 1) and (shape[1] == 1 or s.stride(1) == shape[0]):
-        return s
-    return s.t().contiguous().t()
+    if s.device != like.device:
+        raise ValueError(f"tensors must be on one device, not {like.device} and {s.device}")
+    if s.shape != (row_blocks, col_blocks):
+        raise ValueError(f"{name} must have shape {(row_blocks, col_blocks)}, not {tuple(s.shape)}")
+    along, across = s.stride()
+    if (row_blocks > 1 and along != 1) or (col_blocks > 1 and across != row_blocks):
+        s = s.t().contiguous().t()
+    return s
 
 
-def _weight_block(q, s, name: str) -> int:
-    """128 or 1, by which of the two shapes of scales `s` has for the codes `q`."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 2 or not isinstance(s, torch.Tensor) or s.dim() != 2:
-        raise TypeError(f"{name} and its scale must be matrices")
-    return BLOCK if s.shape[0] == _up(q.shape[0], BLOCK) else 1
-
-
-def _same_device(first, *others) -> None:
-    for t in others:
-        if t.device != first.device:
-            raise ValueError(f"tensors must be on one device, not {first.device} and {t.device}")
-
-
-def _matmul(a, a_scale, b, b_scale, b_rows: int, out_dtype) -> torch.Tensor:
-    (m, k), n = a.shape, b.shape[0]
-    out = torch.empty((m, n), dtype=out_dtype, device=a.device)
-    _call(abi.load().fp8_block_matmul, a.device, a.data_ptr(), _code_distance(a), a_scale.data_ptr(), b.data_ptr(),
-          _code_distance(b), b_scale.data_ptr(), b_rows, m, n, k, out.data_ptr(), _TYPES[out_dtype], max(n, 1))
-    return out
+def _weights(q, s, name: str):
+    """(q, rows, columns, distance of rows, scales, rows of a block) of a product's second operand: its scales' shape
+    says whether a block is 128 rows or one."""
+    q, rows, cols, ld = _codes(q, name)
+    if not isinstance(s, torch.Tensor) or s.dim() != 2:
+        raise TypeError(f"{name}_scale must be a float32 CUDA (HIP) matrix")
+    square = (rows + 127) // 128
+    if s.shape[0] == square:
+        return q, rows, cols, ld, _scales(s, square, (cols + 127) // 128, q, name + "_scale"), BLOCK
+    return q, rows, cols, ld, _scales(s, rows, (cols + 127) // 128, q, name + "_scale"), 1
 
 
 def fp8_block_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor, *,
                      out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """a b^T [M, N] of two block-quantized matrices a [M, K] and b [N, K] (see ``fp8_block_quantize``).  a_scale is
-    [M, ceil(K / 128)]; b_scale is [ceil(N / 128), ceil(K / 128)] or [N, ceil(K / 128)].  Blocks are summed in float32
-    and joined in float32."""
-    _type(out_dtype, "out_dtype")
-    a, b_rows, b = _codes(a, "a"), _weight_block(b, b_scale, "b"), _codes(b, "b")
-    if a.shape[1] != b.shape[1]:
-        raise ValueError(f"a and b must have rows of one length, not {a.shape[1]} and {b.shape[1]}")
-    a_scale, b_scale = _scales(a_scale, a, 1, "a_scale"), _scales(b_scale, b, b_rows, "b_scale")
-    _same_device(a, a_scale, b, b_scale)
-    return _matmul(a, a_scale, b, b_scale, b_rows, out_dtype)
+    [M, ceil(K / 128)]; b_scale is [ceil(N / 128), ceil(K / 128)] or [N, ceil(K / 128)].  A float32 result comes from
+    exact products summed in float32; for a 16-bit result the 8-bit matrix instruction sums the products of a block, with
+    an error under the result's own rounding."""
+    out_type = _type(out_dtype, "out_dtype")
+    a, m, k, ld_a = _codes(a, "a")
+    b, n, k_b, ld_b, b_scale, b_rows = _weights(b, b_scale, "b")
+    if k != k_b:
+        raise ValueError(f"a and b must have rows of one length, not {k} and {k_b}")
+    a_scale = _scales(a_scale, m, (k + 127) // 128, a, "a_scale")
+    dev = a.device
+    if b.device != dev:
+        raise ValueError(f"tensors must be on one device, not {dev} and {b.device}")
+    out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    _call(_entry().fp8_block_matmul, dev.index, a.data_ptr(), ld_a, a_scale.data_ptr(), b.data_ptr(), ld_b,
+          b_scale.data_ptr(), b_rows, m, n, k, out.data_ptr(), out_type, n or 1)
+    return out
 
 
-def _tokens(x, k: int) -> torch.Tensor:
+def _tokens(x, k: int, w: torch.Tensor):
+    """_matrix of x [..., k] as rows, on w's device."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA (HIP) tensor")
     if x.dim() < 1 or x.shape[-1] != k:
         raise ValueError(f"x must be [..., {k}], not {tuple(x.shape)}")
-    if x.dim() != 2:
-        x = x.reshape(x.shape[:-1].numel(), k)
-    return _matrix(x, "x")
+    if x.device != w.device:
+        raise ValueError(f"tensors must be on one device, not {x.device} and {w.device}")
+    return _matrix(x if x.dim() == 2 else x.reshape(x.shape[:-1].numel(), k), "x")
 
 
 def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor) -> torch.Tensor:
     """y [..., N] = x w^T in x's type, for weights w [N, K] quantized before (``fp8_block_quantize(weights,
     block_rows=128)``); x [..., K] is quantized on the way, a scale for each 128 of a row."""
-    b_rows, w = _weight_block(w, w_scale, "w"), _codes(w, "w")
-    w_scale = _scales(w_scale, w, b_rows, "w_scale")
-    n, k = w.shape
-    rows = _tokens(x, k)
-    _same_device(x, w, w_scale)
-    m, dev, lib = rows.shape[0], x.device, abi.load()
-    y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=dev)
+    w, n, k, ld_w, w_scale, b_rows = _weights(w, w_scale, "w")
+    rows, x_type, m, _, ld_x = _tokens(x, k, w)
+    dev, lib = w.device, _entry()
+    y = torch.empty((m, n) if x.dim() == 2 else (*x.shape[:-1], n), dtype=x.dtype, device=dev)
     need = lib.fp8_linear_quantized_workspace_bytes(m, k)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call(lib.fp8_linear_quantized, dev, rows.data_ptr(), _TYPES[x.dtype], m, _row_distance(rows), w.data_ptr(),
-          _code_distance(w), w_scale.data_ptr(), b_rows, n, k, y.data_ptr(), max(n, 1), _ptr(ws), need)
+    ws = _bytes(need, dev)
+    _call(lib.fp8_linear_quantized, dev.index, rows.data_ptr(), x_type, m, ld_x, w.data_ptr(), ld_w, w_scale.data_ptr(),
+          b_rows, n, k, y.data_ptr(), n or 1, _ptr(ws), need)
     return y
 
 
@@ -193,14 +205,14 @@ def _bytes(n: int, device) -> torch.Tensor | None:
 
 def _linear_forward(x, w, grads: int):
     """(y, what the backward of `grads` needs): x [..., K] and w [N, K]."""
-    n, k = w.shape
-    rows = _tokens(x, k)
-    m, dev, lib = rows.shape[0], x.device, abi.load()
+    w, w_type, n, k, ld_w = _matrix(w, "w")
+    rows, x_type, m, _, ld_x = _tokens(x, k, w)
+    dev, lib = w.device, _entry()
     y = torch.empty((*x.shape[:-1], n), dtype=x.dtype, device=dev)
     keep, need = lib.fp8_linear_saved_bytes(m, n, k, grads), lib.fp8_linear_workspace_bytes(m, n, k)
     saved, ws = _bytes(keep, dev), _bytes(need, dev)
-    _call(lib.fp8_linear_forward, dev, rows.data_ptr(), _TYPES[x.dtype], m, _row_distance(rows), w.data_ptr(),
-          _TYPES[w.dtype], n, _row_distance(w), k, grads, y.data_ptr(), max(n, 1), _ptr(saved), keep, _ptr(ws), need)
+    _call(lib.fp8_linear_forward, dev.index, rows.data_ptr(), x_type, m, ld_x, w.data_ptr(), w_type, n, ld_w, k, grads,
+          y.data_ptr(), n or 1, _ptr(saved), keep, _ptr(ws), need)
     return y, saved
 
 
@@ -221,15 +233,15 @@ class _Fp8Linear(torch.autograd.Function):
     def backward(ctx, dy):
         (saved,) = ctx.saved_tensors
         x_shape, x_type, (n, k), w_type, grads = ctx.like
-        rows, dev, lib = _tokens(dy, n), dy.device, abi.load()
-        m = rows.shape[0]
+        rows, dy_type, m, _, ld_dy = _tokens(dy, n, dy)
+        dev, lib = dy.device, _entry()
         dx = torch.empty(x_shape, dtype=x_type, device=dev) if grads & abi.BCJR_GRAD_X else None
         dw = torch.empty((n, k), dtype=w_type, device=dev) if grads & abi.BCJR_GRAD_W else None
         need = lib.fp8_linear_workspace_bytes(m, n, k)
         ws = _bytes(need, dev)
-        _call(lib.fp8_linear_backward, dev, rows.data_ptr(), _TYPES[x_type], m, _row_distance(rows), n, k, grads,
-              _ptr(saved), 0 if saved is None else saved.numel(), _ptr(dx), max(k, 1), _ptr(dw), _TYPES[w_type],
-              max(k, 1), _ptr(ws), need)
+        _call(lib.fp8_linear_backward, dev.index, rows.data_ptr(), dy_type, m, ld_dy, n, k, grads, _ptr(saved),
+              0 if saved is None else saved.numel(), _ptr(dx), k or 1, _ptr(dw), _TYPES[w_type], k or 1, _ptr(ws),
+              need)
         return dx, dw
 
 
@@ -237,9 +249,8 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     """y [..., N] = x w^T in x's type as a differentiable function of x [..., K] and w [N, K], every product in 8 bits:
     x and the upstream gradient are quantized with a scale for each 128 along the sum they enter, w with one for each
     128 x 128.  dx has x's type and dw has w's.  w may be the soft codeword (``soft_quantize``) of a layer's weights."""
-    w = _matrix(w, "w")
-    _tokens(x, w.shape[1])
-    _same_device(x, w)
+    if not isinstance(x, torch.Tensor) or not isinstance(w, torch.Tensor):
+        raise TypeError("x and w must be CUDA (HIP) tensors")
     if torch.is_grad_enabled() and (x.requires_grad or w.requires_grad):
         return _Fp8Linear.apply(x, w)
     return _linear_forward(x, w, 0)[0]
@@ -266,10 +277,10 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
     if (cols > 1 and g3.stride(2) != 1 or rows > 1 and g3.stride(1) < cols
             or g3.shape[0] > 1 and g3.stride(0) < 0):
         g3 = g3.contiguous()
-    batch = g3.shape[0]
-    need = abi.load().orthogonalize_workspace_bytes(batch, rows, cols, out_type)
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=g.device)
-    _call(abi.load().orthogonalize, g.device, g3.data_ptr(), in_type, batch, rows, cols, _row_distance(g3),
-          g3.stride(0) if batch > 1 else 0, int(steps), a, b, c, float(eps), out.data_ptr(), out_type, ws.data_ptr(),
-          need)
+    batch, (_, ld, _) = g3.shape[0], g3.stride()
+    dev, lib = g.device, _entry()
+    need = lib.orthogonalize_workspace_bytes(batch, rows, cols, out_type)
+    ws = _bytes(need, dev)
+    _call(lib.orthogonalize, dev.index, g3.data_ptr(), in_type, batch, rows, cols, ld if rows > 1 else cols,
+          g3.stride(0) if batch > 1 else 0, int(steps), a, b, c, float(eps), out.data_ptr(), out_type, _ptr(ws), need)
     return out
