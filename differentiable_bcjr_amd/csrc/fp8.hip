@@ -2,10 +2,10 @@
 // matrices held that way.
 #include "bcjr.h"
 
-#include <hip/hip_bf16.h>
-#include <hip/hip_fp16.h>
+#include <type_traits>
 
 #include "layer_args.hpp"
+#include "layer_types.hpp"
 #include "mfma_tile.hpp"
 
 namespace bcjr {
@@ -21,31 +21,6 @@ namespace {
 
 constexpr float kInvMax = 1.0f / 448.0f;   // 448: the largest e4m3 number
 constexpr float kMinScale = 1.17549435e-38f;
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__hip_bfloat16 x) {
-    return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, x) << 16);
-}
-__device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
-
-// 8 elements from p on, the first `count` of them present (the rest 0).  `wide`: all 8 are, on a 16-byte boundary.
-template <class T>
-__device__ __forceinline__ void load8(const T* p, int count, bool wide, float (&v)[8]) {
-    if (wide) {
-        constexpr int kPer = 16 / sizeof(T);
-#pragma unroll
-        for (int j = 0; j < 8; j += kPer) {
-            const v4i w = *(const v4i*)(p + j);
-            T e[kPer];
-            __builtin_memcpy(e, &w, 16);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) v[j + i] = to_f32(e[i]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < count ? to_f32(p[j]) : 0.0f;
-    }
-}
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
@@ -248,15 +223,6 @@ hipError_t quantize(const QuantizeArgs& a, hipStream_t st) {
 // with the 16-bit instruction on codes widened to halves, which hold every e4m3 number: exact products, float32 sums,
 // at half the rate.
 
-template <class T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ _Float16 from_f32<_Float16>(float x) { return (_Float16)x; }
-template <>
-__device__ __forceinline__ __hip_bfloat16 from_f32<__hip_bfloat16>(float x) { return __float2bfloat16(x); }
-
 // The 32 codes of a fragment as 32 halves, for four 16x16x32 MFMAs.
 struct Halves {
     v8h h[4];
@@ -277,37 +243,45 @@ __device__ __forceinline__ Halves widen(v8i codes) {
     return out;
 }
 
-__device__ __forceinline__ v4f block_product(const Halves& a, const Halves& b) {
-    v4f p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int h = 0; h < 4; ++h) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.h[h], b.h[h], p, 0, 0, 0);
-    return p;
-}
-
 __device__ __forceinline__ v4f block_product(v8i a, v8i b) {
     const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
 }
 
-template <bool kWide>
-struct Fragment {
-    v8i v;
-    __device__ __forceinline__ void set(v8i codes) { v = codes; }
-};
-template <>
-struct Fragment<true> {
-    Halves v;
-    __device__ __forceinline__ void set(v8i codes) { v = widen(codes); }
-};
+// The block products of one fragment of a with each of b's.
+template <int TN>
+__device__ __forceinline__ void block_products(const v8i (&b)[TN], v8i a, v4f (&p)[TN]) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) p[j] = block_product(b[j], a);
+}
 
-template <class T, int BM, int BN, int WAVES_M, int WAVES_N, bool kRowScales>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(ProductArgs a, int tiles_m, int tiles_n) {
+template <int TN>
+__device__ __forceinline__ void block_products(const Halves (&b)[TN], const Halves& a, v4f (&p)[TN]) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) p[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j].h[h], a.h[h], p[j], 0, 0, 0);
+}
+
+__device__ __forceinline__ void take(v8i codes, v8i& out) { out = codes; }
+__device__ __forceinline__ void take(v8i codes, Halves& out) { out = widen(codes); }
+
+// A stage of the k loop in LDS: the slabs of BM rows of a and BN rows of b, and the scales of those rows' blocks (b's
+// once for each row, also where a block is 128 rows).
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kWavesPerSimd, bool kRowScales>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, kWavesPerSimd) void product_kernel(ProductArgs a, int tiles_m,
+                                                                                        int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
     constexpr bool kWide = sizeof(T) == 4;
-    constexpr bool kPaced = !kWide && !kRowScales;   // the order of MFMAs and multiply-adds is prescribed
     constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
+    constexpr int kScalesAt = (BM + BN) * kSlab, kStageBytes = kScalesAt + (BM + BN) * 4;
+    constexpr int kScaleLoads = (BM + BN) / 64;   // of 64 scales each; waves beyond that repeat one
+    static_assert(kScaleLoads <= kWaves, "one load of scales a wave");
     static_assert(kRowScales || 128 % (BN / WAVES_N) == 0, "a wave's columns lie in one block of b");
-    __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kSlab];
+    using Frag = std::conditional_t<kWide, Halves, v8i>;
+    __shared__ __align__(1024) uint8_t lds[kStages * kStageBytes];
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
@@ -318,16 +292,34 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
     const uint8_t* pb = a.b + (int64_t)n0 * a.ld_b;
     const int rows_a = a.m - m0, rows_b = a.n - n0;
     const int r16 = lane & 15, g = lane >> 4;
+    const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
 
-    SlabSource<BM, kWaves> src_a;
-    SlabSource<BN, kWaves> src_b;
+    using SourceA = SlabSource<BM, kWaves>;
+    using SourceB = SlabSource<BN, kWaves>;
+    SourceA src_a;
+    SourceB src_b;
     src_a.set(pa, (uint32_t)a.ld_a, rows_a, wave, lane);
     src_b.set(pb, (uint32_t)a.ld_b, rows_b, wave, lane);
 
-    const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
-    const int m_first = m0 + wm0 + r16;   // rows of a whose scales this lane applies: m_first + 16 i
-    const int sb_len = kRowScales ? a.n : (a.n + 127) / 128;
-    const int sb_at = kRowScales ? 0 : min((n0 + wn0) / 128, sb_len - 1);
+    // this wave's 64 scales of a stage
+    const int part = wave % kScaleLoads;
+    const float* scales;
+    uint32_t scale_step, scale_lane;
+    if (part < BM / 64) {
+        scales = a.a_scale;
+        scale_step = (uint32_t)a.m;
+        scale_lane = (uint32_t)min(m0 + part * 64 + lane, a.m - 1);
+    } else {
+        const int n = min(n0 + (part - BM / 64) * 64 + lane, a.n - 1);
+        scales = a.b_scale;
+        scale_step = kRowScales ? (uint32_t)a.n : (uint32_t)((a.n + 127) / 128);
+        scale_lane = (uint32_t)(kRowScales ? n : n / 128);
+    }
+    auto fetch_scales = [&](int s, uint8_t* stage) {
+        uint32_t at = scale_lane * 4;
+        asm("" : "+v"(at));
+        load4_to_lds((const uint8_t*)(scales + (int64_t)s * scale_step) + at, stage + kScalesAt + part * 256);
+    };
 
     v4f acc[TM][TN];
 #pragma unroll
@@ -335,56 +327,42 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // The scales of a slab are loaded ahead of the next slab's operands, a step before their use: loads complete in
-    // order, so a load behind the operands would be waited for with them.
-    float sa_next[TM], sb_next[kRowScales ? TN : 1][4];
-    auto fetch_scales = [&](int s) {
-        const float* pa_s = a.a_scale + (int64_t)s * a.m;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sa_next[i] = pa_s[min(m_first + i * 16, a.m - 1)];
-        if constexpr (kRowScales) {
-            const float* pb_s = a.b_scale + (int64_t)s * a.n;
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sb_next[j][e] = pb_s[min(n0 + wn0 + j * 16 + g * 4 + e, a.n - 1)];
-        } else {
-            sb_next[0][0] = a.b_scale[(int64_t)s * sb_len + sb_at];
-        }
-    };
-
     // One slab: the fragments of b stay in registers, those of a pass through one ahead of their use, and a row of
     // tiles' sums are scaled and added while the next row's MFMAs run (a lone MFMA followed by the use of its result
-    // would leave the matrix core idle for its latency).
-    float sa[TM], sb[kRowScales ? TN : 1][4];
-    auto take_scales = [&] {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = kRowScales ? sa_next[i] : sa_next[i] * sb_next[0][0];
-        if constexpr (kRowScales) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sb[j][e] = sb_next[j][e];
-        }
-    };
+    // would leave the matrix core idle for its latency).  The order is prescribed: left to itself the compiler puts
+    // each use right behind its MFMA.
     auto multiply = [&](const uint8_t* la) {
         const uint8_t* lb = la + BM * kSlab;
-        Fragment<kWide> fb[TN];
-        v8i fa[2];
+        const float* ls = (const float*)(la + kScalesAt);
+        Frag fb[TN], fa[2];
+        float sa[TM];
+        v4f sb[kRowScales ? TN : 1];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fb[j].set(read_slab(lb, wn0 + j * 16 + r16, g));
-        fa[0] = read_slab(la, wm0 + r16, g);
+        for (int j = 0; j < TN; ++j) take(read_slab(lb, wn0 + j * 16 + r16, g), fb[j]);
+        take(read_slab(la, wm0 + r16, g), fa[0]);
+        v8i raw;   // codes that are yet to be widened
+        if constexpr (kWide && TM > 1) raw = read_slab(la, wm0 + 16 + r16, g);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = ls[wm0 + i * 16 + r16];
+        if constexpr (kRowScales) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) sb[j] = *(const v4f*)(ls + BM + wn0 + j * 16 + g * 4);
+        } else {
+            const float b = ls[BM + wn0];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) sa[i] *= b;
+        }
         v4f p[2][TN];
-        if constexpr (kPaced) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i <= TM; ++i) {
-            if (i + 1 < TM) fa[(i + 1) & 1] = read_slab(la, wm0 + (i + 1) * 16 + r16, g);
-            if (i < TM) {
-                Fragment<kWide> f;
-                f.set(fa[i & 1]);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) p[i & 1][j] = block_product(fb[j].v, f.v);
+            if constexpr (kWide) {
+                if (i + 1 < TM) take(raw, fa[(i + 1) & 1]);
+                if (i + 2 < TM) raw = read_slab(la, wm0 + (i + 2) * 16 + r16, g);
+            } else {
+                if (i + 1 < TM) take(read_slab(la, wm0 + (i + 1) * 16 + r16, g), fa[(i + 1) & 1]);
             }
+            if (i < TM) block_products(fb, fa[i & 1], p[i & 1]);
             if (i > 0) {
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
@@ -397,52 +375,49 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
                             acc[i - 1][j][e] = fmaf(v, sa[i - 1], acc[i - 1][j][e]);
                     }
             }
-            if constexpr (kPaced) {
-                if (i + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // the next fragment of a
+            // the next fragment's reads, then MFMAs with an even share of the multiply-adds (and widenings) after each
+            constexpr int kMfma = kWide ? 4 * TN : TN;
+            constexpr int kScale = (kRowScales ? 8 : 4) * TN, kWiden = kWide ? 16 : 0;
+            const int valu = (i > 0 ? kScale : 0) + (i + 1 < TM ? kWiden : 0);
+            if (!kWide && i + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            if (i < TM) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    if (i < TM) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);     // one MFMA
-                    if (i > 0) __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);      // four multiply-adds
+                for (int x = 0; x < kMfma; ++x) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    if (valu == kScale + kWiden) __builtin_amdgcn_sched_group_barrier(0x2, (kScale + kWiden) / kMfma, 0);
+                    else if (valu == kScale) __builtin_amdgcn_sched_group_barrier(0x2, kScale / kMfma, 0);
+                    else if (valu == kWiden && kWiden) __builtin_amdgcn_sched_group_barrier(0x2, kWiden ? kWiden / kMfma : 1, 0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
+            if (kWide && i + 2 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
     const int full = a.k / kSlab, tail = a.k % kSlab;
-    if (full > 0) {
-        fetch_scales(0);
-        src_a.fetch(0, lds[0], wave);
-        src_b.fetch(0, lds[0] + BM * kSlab, wave);
-    }
-    for (int s = 0; s < full; ++s) {
-        wait_loads();
-        __syncthreads();   // slab s is in LDS, and nobody reads the other buffer any more
-        const uint8_t* now = lds[s & 1];
-        take_scales();
-        if (s + 1 < full) {
-            fetch_scales(s + 1);
-            uint8_t* next = lds[(s + 1) & 1];
-            src_a.fetch((uint32_t)(s + 1) * kSlab, next, wave);
-            src_b.fetch((uint32_t)(s + 1) * kSlab, next + BM * kSlab, wave);
-        }
-        multiply(now);
-    }
+    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + 1>(
+        full,
+        [&](int s, int slot) {
+            uint8_t* stage = lds + slot * kStageBytes;
+            src_a.fetch((uint32_t)s * kSlab, stage, wave);
+            src_b.fetch((uint32_t)s * kSlab, stage + BM * kSlab, wave);
+            fetch_scales(s, stage);
+        },
+        [&](int slot) { multiply(lds + slot * kStageBytes); });
     if (tail) {
-        __syncthreads();
-        fetch_scales(full);
-        fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, (uint32_t)full * kSlab, tail, lds[0], wave, lane);
-        fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, (uint32_t)full * kSlab, tail, lds[0] + BM * kSlab, wave,
-                               lane);
-        __syncthreads();
-        take_scales();
-        multiply(lds[0]);
+        meet();
+        fetch_scales(full, lds);
+        fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, lds, wave, lane);
+        fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, lds + BM * kSlab, wave, lane);
+        wait_loads<0>();
+        meet();
+        multiply(lds);
     }
 
     using Tile = WaveTile<T, TM * 16, TN * 16>;
     static_assert(kWaves * Tile::kBytes <= (int)sizeof(lds), "every wave's results fit in LDS");
-    __syncthreads();   // nobody reads the operands any more
-    uint8_t* mine = lds[0] + wave * Tile::kBytes;
+    meet();   // nobody reads the operands any more
+    uint8_t* mine = lds + wave * Tile::kBytes;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -465,14 +440,6 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void product_kernel(Product
 // 64-byte sectors), the workgroup's waves share the slabs of those rows among them, four slabs of each in flight, and
 // their sums meet in LDS in a fixed order.  a either comes as codes or as numbers that are quantized in the operand's
 // registers: the four lanes of a row hold its whole block, so its largest entry is two lane exchanges away.
-
-// Chunk `at` .. at + 15 of a row of k codes, zeros behind its end.
-__device__ __forceinline__ v4i load_chunk(const uint8_t* row, int at, int k) {
-    if (at + 16 <= k) return *(const v4i*)(row + at);
-    uint32_t w[4] = {0, 0, 0, 0};
-    for (int b = 0; b < k - at; ++b) w[b >> 2] |= (uint32_t)row[at + b] << ((b & 3) * 8);
-    return v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-}
 
 __device__ __forceinline__ v8i load_slab(const uint8_t* row, int at, int g, int k) {
     return __builtin_shufflevector(load_chunk(row, at + g * 16, k), load_chunk(row, at + 64 + g * 16, k), 0, 1, 2, 3, 4,
@@ -551,10 +518,12 @@ __global__ __launch_bounds__(1024) void few_rows_kernel(ProductArgs a, int wide)
             } else {
                 fa = quantize_slab(a_row, s * kSlab, g, a.k, have, wide != 0, sa);
             }
-            Fragment<kWide> wa, wb;
-            wa.set(fa);
-            wb.set(fb[u]);
-            const v4f p = block_product(wb.v, wa.v);
+            std::conditional_t<kWide, Halves, v8i> wa, wb[1];
+            take(fa, wa);
+            take(fb[u], wb[0]);
+            v4f sums4[1];
+            block_products(wb, wa, sums4);
+            const v4f p = sums4[0];
             const float* sb = a.b_scale + (int64_t)s * sb_len;
             if constexpr (kRowScales) {
 #pragma unroll
@@ -590,34 +559,35 @@ void few_rows(const ProductArgs& a, hipStream_t st) {
         few_rows_kernel<T, X, false><<<grid, waves * 64, 0, st>>>(a, wide);
 }
 
-template <class T, int BM, int BN, int WAVES_M, int WAVES_N>
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kWavesPerSimd, bool kRows = true>
 void product_tiles(const ProductArgs& a, hipStream_t st) {
     const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
     const unsigned grid = (unsigned)tm * (unsigned)tn;
     constexpr int kThreads = 64 * WAVES_M * WAVES_N;
-    if (a.b_rows == 1)
-        product_kernel<T, BM, BN, WAVES_M, WAVES_N, true><<<grid, kThreads, 0, st>>>(a, tm, tn);
-    else
-        product_kernel<T, BM, BN, WAVES_M, WAVES_N, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
+    if constexpr (kRows) {
+        if (a.b_rows == 1) {
+            product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kWavesPerSimd, true>
+                <<<grid, kThreads, 0, st>>>(a, tm, tn);
+            return;
+        }
+    }
+    product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kWavesPerSimd, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
 }
 
 template <class T>
 hipError_t product(const ProductArgs& a, hipStream_t st) {
-    const auto tiles = [&](int64_t size) { return ((a.m + size - 1) / size) * ((a.n + size - 1) / size); };
+    const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
     if (a.m <= kFewRows) {
         few_rows<T, uint8_t>(a, st);
-        return hipGetLastError();
+    } else if (sizeof(T) == 2 && a.b_rows == 128 && tiles(256, 256) >= 256) {
+        if constexpr (sizeof(T) == 2) product_tiles<T, 256, 256, 2, 4, 2, 2, false>(a, st);
+    } else if (tiles(256, 128) >= 256) {
+        product_tiles<T, 256, 128, 4, 2, 3, 2>(a, st);
+    } else if (tiles(128, 128) >= 256) {
+        product_tiles<T, 128, 128, 2, 2, 2, 2>(a, st);
+    } else {
+        product_tiles<T, 64, 64, 2, 2, 4, 2>(a, st);
     }
-    if constexpr (sizeof(T) == 2) {
-        if (tiles(256) >= 256) {
-            product_tiles<T, 256, 256, 2, 4>(a, st);
-            return hipGetLastError();
-        }
-    }
-    if (tiles(128) >= 256)
-        product_tiles<T, 128, 128, 2, 2>(a, st);
-    else
-        product_tiles<T, 64, 64, 2, 2>(a, st);
     return hipGetLastError();
 }
 

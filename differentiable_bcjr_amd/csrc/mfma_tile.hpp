@@ -32,8 +32,49 @@ __device__ __forceinline__ void load_to_lds(const void* g, void* lds) {
                                      (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
 }
 
-// Every load this wave has issued is complete (those to LDS too, which a barrier alone does not wait for).
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// 4 bytes per lane, the same way.
+__device__ __forceinline__ void load4_to_lds(const void* g, void* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                     (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
+}
+
+// All but the last `kPending` loads this wave has issued are complete (loads to LDS too, which a barrier alone does not
+// wait for; loads complete in order).
+template <int kPending>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(kPending >= 0 && kPending < 64, "a 6-bit count");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPending) : "memory");
+}
+
+// The workgroup's waves meet; none of what comes after is moved ahead of it, nor what came before behind it.
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The k loop: stage s of `total` is loaded into LDS slot s mod kStages, kStages - 1 stages ahead of its use.  `issue`
+// issues kLoads loads in every wave and no others are in flight; `use` reads the slot.  One meeting a stage: behind it
+// the stage is there for all waves (each has waited for its own loads), and the slot that is loaded next is no longer
+// read (it was used in the step before).
+template <int kStages, int kLoads, class Issue, class Use>
+__device__ __forceinline__ void pipelined(int total, Issue issue, Use use) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s)
+        if (s < total) issue(s, s);
+    int slot = 0;
+#pragma unroll 1
+    for (int s = 0; s < total; ++s) {
+        if (s + kStages - 1 <= total)
+            wait_loads<kLoads*(kStages - 2)>();
+        else
+            wait_loads<0>();
+        meet();
+        if (s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+        use(slot);
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+}
 
 // ROWS rows of an operand, of which NW waves fetch one slab after the other: lane l of a wave's i-th instruction brings
 // 16 bytes of row 8 (i NW + wave) + l / 8.  Rows from `rows` on repeat the last one (their results are not stored).  The
@@ -65,26 +106,32 @@ struct SlabSource {
     }
 };
 
-// The last slab of a row length that is no multiple of 128: `valid` bytes are there, the rest is written as zeros.
+// Bytes at .. at + 15 of a row of `length` bytes that starts at `row`, zeros behind its end.  The row starts on a
+// 16-byte boundary.  In the chunk that the end cuts, each byte is loaded by itself (sixteen independent loads).
+__device__ __forceinline__ v4i load_chunk(const uint8_t* row, int at, int length) {
+    v4i v = {0, 0, 0, 0};
+    if (at + 16 <= length) {
+        v = *(const v4i*)(row + at);
+    } else if (at < length) {
+        uint32_t byte[16];
+#pragma unroll
+        for (int b = 0; b < 16; ++b) byte[b] = row[min(at + b, length - 1)];
+#pragma unroll
+        for (int b = 0; b < 16; ++b) v[b >> 2] |= (int)(at + b < length ? byte[b] << ((b & 3) * 8) : 0u);
+    }
+    return v;
+}
+
+// The slab behind the last whole one of a row of `length` bytes (kbyte: where it begins).
 template <int ROWS, int NW>
-__device__ __forceinline__ void fetch_tail(const uint8_t* base, uint32_t ld, int rows, uint32_t kbyte, int valid,
+__device__ __forceinline__ void fetch_tail(const uint8_t* base, uint32_t ld, int rows, int kbyte, int length,
                                            uint8_t* lds, int wave, int lane) {
 #pragma unroll 1
     for (int i = 0; i < ROWS / (8 * NW); ++i) {
         const int part = i * NW + wave;
         const int row = part * 8 + (lane >> 3);
-        const int r = row < rows ? row : rows - 1;
-        const int at = (int)slab_chunk(row, lane & 7) * 16;
-        const uint8_t* p = base + ((size_t)((uint32_t)r * (uint64_t)ld) + kbyte + at);
-        v4i v = {0, 0, 0, 0};
-        if (at + 16 <= valid) {
-            v = *(const v4i*)p;
-        } else if (at < valid) {
-            uint32_t w[4] = {0, 0, 0, 0};
-            for (int b = 0; b < valid - at; ++b) w[b >> 2] |= (uint32_t)p[b] << ((b & 3) * 8);
-            v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-        }
-        *(v4i*)(lds + part * 1024 + lane * 16) = v;
+        const uint8_t* p = base + (size_t)((uint32_t)min(row, rows - 1) * ld);
+        *(v4i*)(lds + part * 1024 + lane * 16) = load_chunk(p, kbyte + (int)slab_chunk(row, lane & 7) * 16, length);
     }
 }
 

@@ -13,10 +13,10 @@
 // and the result is as near the exact one as that of float32 products.
 #include "bcjr.h"
 
-#include <hip/hip_bf16.h>
-#include <hip/hip_fp16.h>
+#include <algorithm>
 
 #include "layer_args.hpp"
+#include "layer_types.hpp"
 #include "mfma_tile.hpp"
 
 namespace bcjr {
@@ -30,56 +30,16 @@ constexpr int kPartials = 256;  // partial sums of |G|^2 per matrix
 __host__ __device__ inline int64_t pad_up(int64_t v) { return (v + kPad - 1) / kPad * kPad; }
 inline size_t area(size_t bytes) { return (bytes + 255) & ~(size_t)255; }
 
+struct Cut;
+inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, bool symmetric, int slab_cols);
+
 struct Layout {
     int64_t m, n, mp, np;   // m <= n, and padded
     bool tall, split;
-    size_t partials, x_hi, x_lo, xt_hi[2], xt_lo[2], a_hi, a_lo, b_hi, b_lo, total;
+    size_t partials, x, x_lo, xt[2], a, b, sums, total;   // offsets in the workspace
 };
 
-Layout make_layout(int64_t batch, int64_t rows, int64_t cols, int32_t out_type) {
-    Layout l{};
-    l.tall = rows > cols;
-    l.m = l.tall ? cols : rows;
-    l.n = l.tall ? rows : cols;
-    l.mp = pad_up(l.m);
-    l.np = pad_up(l.n);
-    l.split = out_type != BCJR_TYPE_BF16;
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-        const size_t here = at;
-        at += area(bytes);
-        return here;
-    };
-    const size_t x = (size_t)batch * l.mp * l.np * 2, s = (size_t)batch * l.mp * l.mp * 2;
-    l.partials = take((size_t)batch * kPartials * 8);
-    l.x_hi = take(x);
-    l.x_lo = take(x);
-    for (int i = 0; i < 2; ++i) {
-        l.xt_hi[i] = take(x);
-        l.xt_lo[i] = l.split ? take(x) : 0;
-    }
-    l.a_hi = take(s);
-    l.a_lo = l.split ? take(s) : 0;
-    l.b_hi = take(s);
-    l.b_lo = l.split ? take(s) : 0;
-    l.total = at;
-    return l;
-}
-
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__hip_bfloat16 x) {
-    return __uint_as_float((uint32_t)__builtin_bit_cast(uint16_t, x) << 16);
-}
-__device__ __forceinline__ float to_f32(_Float16 x) { return (float)x; }
-
-template <class T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ _Float16 from_f32<_Float16>(float x) { return (_Float16)x; }
-template <>
-__device__ __forceinline__ __hip_bfloat16 from_f32<__hip_bfloat16>(float x) { return __float2bfloat16(x); }
+Layout make_layout(int64_t batch, int64_t rows, int64_t cols, int32_t out_type);
 
 // ---------------------------------------------------------------- the norm
 //
@@ -98,17 +58,34 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
     return lds[0] + lds[1] + lds[2] + lds[3];
 }
 
+constexpr int kSumAhead = 4;   // loads of eight elements that a thread has in flight
+
 template <class T>
-__global__ __launch_bounds__(256) void square_sum_kernel(const T* g, int64_t rows, int64_t cols, int64_t ld,
-                                                         int64_t batch_stride, double* partials) {
+__global__ __launch_bounds__(256) void square_sum_kernel(const T* g, int rows, int cols, int64_t ld,
+                                                         int64_t batch_stride, int wide, double* partials) {
     __shared__ double lds[4];
     const T* p = g + (int64_t)blockIdx.y * batch_stride;
+    const uint32_t across = (uint32_t)(cols + 7) / 8, count = across * (uint32_t)rows, step = gridDim.x * 256;
     double sum = 0.0;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256) {
-            const double v = (double)to_f32(p[r * ld + c]);
-            sum += v * v;
+    for (uint32_t at = blockIdx.x * 256 + threadIdx.x; at < count; at += step * kSumAhead) {
+        float v[kSumAhead][8];
+#pragma unroll
+        for (int u = 0; u < kSumAhead; ++u) {
+            const uint32_t i = at + u * step;
+            const int col = i < count ? (int)(i % across) * 8 : cols;
+            const int left = cols - col;
+            if (left > 0) {
+                load8(p + (int64_t)(i / across) * ld + col, left, wide && left >= 8, v[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+            }
         }
+#pragma unroll
+        for (int u = 0; u < kSumAhead; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fma((double)v[u][j], (double)v[u][j], sum);
+    }
     sum = block_sum(sum, lds);
     if (threadIdx.x == 0) partials[(int64_t)blockIdx.y * kPartials + blockIdx.x] = sum;
 }
@@ -118,15 +95,15 @@ __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
     lo = (_Float16)(v - (float)hi);
 }
 
-// G's tile of 64 x 64, normalised and scaled: as it lies into `direct`, transposed into `turned`.
-template <class T>
+// G's tile of 64 x 64, normalised and scaled: as it lies into `direct`, transposed into `turned`, each in the layout of
+// the products' operands.  lo: X's lo halves where they lie apart, on the side that X is (kSplit: unused).
+template <class T, bool kSplit>
 __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows, int64_t cols, int64_t ld,
-                                                        int64_t batch_stride, const double* partials, int parts,
-                                                        float eps, _Float16* direct_hi, _Float16* direct_lo,
-                                                        _Float16* turned_hi, _Float16* turned_lo, int64_t rows_p,
-                                                        int64_t cols_p) {
+                                                        int64_t batch_stride, int wide, const double* partials,
+                                                        int parts, float eps, _Float16* direct, _Float16* turned,
+                                                        _Float16* lo_out, int tall, int64_t rows_p, int64_t cols_p) {
     __shared__ double lds[4];
-    __shared__ uint32_t tile[64][65];
+    __shared__ uint32_t tile[64][65];   // hi | lo << 16
     const int t = threadIdx.x;
     const int64_t item = blockIdx.z;
     const double total = block_sum(t < parts ? partials[item * kPartials + t] : 0.0, lds);
@@ -134,47 +111,234 @@ __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows
     const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
     const T* p = g + item * batch_stride;
     const int64_t base = item * rows_p * cols_p;
+    // 16 neighbours of a row of the result, from column 16 q of the tile on
+    const auto put = [&](_Float16* to, int64_t row, int64_t row_length, int64_t col, const uint32_t (&w)[16], bool lo_here) {
+        v4i hi[2], lo[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int r = i * 4 + (t >> 6), c = t & 63;
-        float v = 0.0f;
-        if (r0 + r < rows && c0 + c < cols) v = to_f32(p[(r0 + r) * ld + c0 + c]) / norm * kXScale;
-        _Float16 hi, lo;
-        split(v, hi, lo);
-        if (direct_hi) direct_hi[base + (r0 + r) * cols_p + c0 + c] = hi;
-        if (direct_lo) direct_lo[base + (r0 + r) * cols_p + c0 + c] = lo;
-        tile[r][c] = (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
+        for (int j = 0; j < 8; ++j) {
+            hi[j / 4][j % 4] = (int)((w[2 * j] & 0xffffu) | (w[2 * j + 1] << 16));
+            lo[j / 4][j % 4] = (int)((w[2 * j] >> 16) | (w[2 * j + 1] & 0xffff0000u));
+        }
+        const int64_t at = kSplit ? 2 * (base + row * row_length) + (col >> 5) * 64 + (col & 31)
+                                  : base + row * row_length + col;
+        *(v4i*)(to + at) = hi[0];
+        *(v4i*)(to + at + 8) = hi[1];
+        if (kSplit || lo_here) {
+            _Float16* to_lo = kSplit ? to + 32 : lo_out;
+            *(v4i*)(to_lo + at) = lo[0];
+            *(v4i*)(to_lo + at + 8) = lo[1];
+        }
+    };
+    const int line = t >> 2, q = (t & 3) * 16;
+    uint32_t w[16];
+    const int64_t left = r0 + line < rows ? cols - (c0 + q) : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[8];
+        const int here = (int)min(max(left - h * 8, (int64_t)0), (int64_t)8);
+        if (here > 0) {
+            load8(p + (r0 + line) * ld + c0 + q + h * 8, here, wide && here == 8, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            _Float16 hi, lo;
+            split(j < here ? v[j] / norm * kXScale : 0.0f, hi, lo);
+            w[h * 8 + j] =
+                (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
+        }
     }
+    put(direct, r0 + line, cols_p, c0 + q, w, !tall);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) tile[line][q + j] = w[j];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int c = i * 4 + (t >> 6), r = t & 63;
-        const uint32_t w = tile[r][c];
-        if (turned_hi) turned_hi[base + (c0 + c) * rows_p + r0 + r] = __builtin_bit_cast(_Float16, (uint16_t)(w & 0xffff));
-        if (turned_lo) turned_lo[base + (c0 + c) * rows_p + r0 + r] = __builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
-    }
+    for (int j = 0; j < 16; ++j) w[j] = tile[q + j][line];
+    put(turned, c0 + line, rows_p, r0 + q, w, tall);
 }
 
 // ---------------------------------------------------------------- the products
+//
+// Operands: with kSplit a row holds, for each 32 columns, the 32 hi halves and then the 32 lo halves, so one slab brings
+// both halves of 32 columns and its three products are formed from the same two fragments; without, a row holds the hi
+// halves alone (and X's lo halves lie in an array of their own).  The symmetric products compute the tiles on and below
+// the diagonal and write each twice.
 
 enum Mode { kGram, kPoly, kStep };
 
-struct ProdArgs {
-    const _Float16 *p_hi, *p_lo;   // [rows][k]
-    const _Float16 *q_hi, *q_lo;   // [cols][k]
-    int64_t p_batch, q_batch;      // elements from one matrix of the batch to the next
-    int32_t rows, cols, k;         // multiples of kPad
-    _Float16 *o_hi, *o_lo;         // [rows][cols]; kPoly reads A from a_hi, a_lo, kStep reads X here
-    const _Float16 *a_hi, *a_lo;
-    _Float16 *t_hi, *t_lo;         // kStep: the transpose [cols][rows]
-    int64_t o_batch;
-    float alpha, beta;             // kGram: alpha acc; kPoly: alpha A + beta acc; kStep: alpha X + beta acc
-    void* out;                     // kStep, last: the result
-    int32_t m, n, tall;
-    int64_t out_batch;
+template <bool kSplit>
+struct Halves2 {
+    static constexpr int kPer = kSplit ? 2 : 1;         // halves stored for a column
+    static constexpr int kSlabCols = kSplit ? 32 : 64;  // columns of a slab
+    // where the hi half of column `col` lies in a row; its lo half lies 32 behind (kSplit)
+    static __host__ __device__ __forceinline__ int64_t at(int64_t col) {
+        return kSplit ? (col >> 5) * 64 + (col & 31) : col;
+    }
 };
 
-// The first or second 32 halves of a slab.
+struct ProdArgs {
+    const _Float16 *p, *q;        // [rows][k] and [cols][k]
+    int64_t p_batch, q_batch;     // halves from one matrix of the batch to the next
+    int32_t rows, cols, k;        // multiples of kPad
+    const _Float16 *old, *old_lo; // kPoly: A; kStep: X (old_lo: X's lo halves where they lie apart)
+    _Float16 *o, *o_lo;           // the result [rows][cols]
+    _Float16* t;                  // its transpose [cols][rows]: the same array where it is symmetric
+    int64_t o_batch, lo_batch;
+    float alpha, beta;            // kGram: alpha acc; kPoly, kStep: alpha old + beta acc
+    void* out;                    // kStep, last: the result in its own type, m x n or (tall) n x m
+    int32_t m, n, tall;
+    int64_t out_batch;
+    float* partial;               // more than one part: float32 sums [part][tile][wave][fragment][lane]
+    int32_t parts;                // parts of the k loop
+};
+
+struct TilePlace {
+    int bm, bn;
+};
+
+template <Mode kMode>
+__device__ __forceinline__ TilePlace tile_place(int id, int tiles_m, int tiles_n) {
+    TilePlace p;
+    if constexpr (kMode == kStep) {
+        banded_tile(id, tiles_m, tiles_n, 8, p.bm, p.bn);
+    } else {   // row by row
+        p.bm = (int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
+        while (p.bm * (p.bm + 1) / 2 > id) --p.bm;
+        while ((p.bm + 1) * (p.bm + 2) / 2 <= id) ++p.bm;
+        p.bn = id - p.bm * (p.bm + 1) / 2;
+    }
+    return p;
+}
+
+// A wave's block of TM x TN fragments whose first element is (row0, col0): the result and its transpose from the sums,
+// through this wave's LDS.  A lane's four sums are neighbours along a row.
+template <Mode kMode, bool kSplit, class T, int TM, int TN>
+__device__ __forceinline__ void finish(const ProdArgs& a, v4f (&acc)[TM][TN], int row0, int col0, int64_t item,
+                                       bool mirror, uint8_t* lds, int lane) {
+    using H = Halves2<kSplit>;
+    int r16 = lane & 15, g = lane >> 4;
+    // Places in LDS are computed anew in each pass below: kept from one to the next they take more registers than there
+    // are next to the sums.
+    const auto forget = [&] { asm volatile("" : "+v"(r16), "+v"(g), "+v"(lane)); };
+    forget();
+    const int64_t o = item * a.o_batch;
+    const int64_t ld = (int64_t)a.cols * H::kPer, ld_t = (int64_t)a.rows * H::kPer;
+    constexpr int R = TM * 16, C = TN * 16;
+    static_assert(kPad % R == 0 && kPad % C == 0, "a block lies wholly inside the padded result or outside");
+    if (row0 >= a.rows || col0 >= a.cols) return;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        if constexpr (kMode == kGram) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] *= a.alpha;
+        } else {
+            const int64_t row = row0 + i * 16 + r16;
+            const _Float16* old = a.old + o + row * ld + (int64_t)col0 * H::kPer + g * 4;
+            const _Float16* old_lo = old + 32;
+            if constexpr (!kSplit && kMode == kStep) old_lo = a.old_lo + item * a.lo_batch + row * a.cols + col0 + g * 4;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int at = (int)H::at(j * 16);
+                const v4h hi = *(const v4h*)(old + at);
+                v4h lo = {0, 0, 0, 0};
+                if constexpr (kSplit || kMode == kStep) lo = *(const v4h*)(old_lo + at);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = fmaf(a.alpha, (float)hi[e] + (float)lo[e], a.beta * acc[i][j][e]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // a row's loads at a time: all at once take too many registers
+        }
+    }
+
+    forget();
+    if (kMode == kStep && a.out) {
+        T* out = (T*)a.out + item * a.out_batch;
+        if (a.tall) {
+            using Tile = WaveTile<T, C, R>;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        Tile::put1(lds, j * 16 + g * 4 + e, i * 16 + r16, from_f32<T>(acc[i][j][e] * (1.0f / kXScale)));
+            wave_fence();
+            const bool wide = (uintptr_t)out % 16 == 0 && ((int64_t)a.m * sizeof(T)) % 16 == 0;
+            Tile::store(lds, out + (int64_t)col0 * a.m + row0, a.m, a.n - col0, a.m - row0, wide, lane);
+        } else {
+            using Tile = WaveTile<T, R, C>;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    T v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = from_f32<T>(acc[i][j][e] * (1.0f / kXScale));
+                    Tile::put(lds, i * 16 + r16, j * 16 + g * 4, v);
+                }
+            wave_fence();
+            const bool wide = (uintptr_t)out % 16 == 0 && ((int64_t)a.n * sizeof(T)) % 16 == 0;
+            Tile::store(lds, out + (int64_t)row0 * a.n + col0, a.n, a.m - row0, a.n - col0, wide, lane);
+        }
+        return;
+    }
+
+    {
+        using Tile = WaveTile<_Float16, R, C * H::kPer>;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                _Float16 hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split(acc[i][j][e], hi[e], lo[e]);
+                const int col = (int)H::at(j * 16 + g * 4);
+                Tile::put(lds, i * 16 + r16, col, hi);
+                if constexpr (kSplit) Tile::put(lds, i * 16 + r16, col + 32, lo);
+            }
+        wave_fence();
+        Tile::store(lds, a.o + o + row0 * ld + (int64_t)col0 * H::kPer, ld, R, C * H::kPer, true, lane);
+        wave_fence();
+        if constexpr (!kSplit && kMode == kStep) {   // X's lo halves
+            forget();
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    _Float16 hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split(acc[i][j][e], hi[e], lo[e]);
+                    Tile::put(lds, i * 16 + r16, j * 16 + g * 4, lo);
+                }
+            wave_fence();
+            Tile::store(lds, a.o_lo + item * a.lo_batch + (int64_t)row0 * a.cols + col0, a.cols, R, C, true, lane);
+            wave_fence();
+        }
+    }
+    if (mirror) {
+        forget();
+        using Tile = WaveTile<_Float16, C, R * H::kPer>;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    _Float16 hi, lo;
+                    split(acc[i][j][e], hi, lo);
+                    const int at = (int)H::at(i * 16 + r16);
+                    Tile::put1(lds, j * 16 + g * 4 + e, at, hi);
+                    if constexpr (kSplit) Tile::put1(lds, j * 16 + g * 4 + e, at + 32, lo);
+                }
+        wave_fence();
+        Tile::store(lds, a.t + o + col0 * ld_t + (int64_t)row0 * H::kPer, ld_t, C, R * H::kPer, true, lane);
+        wave_fence();
+    }
+}
+
+// The first or second four registers of a fragment: halves of columns, or with kSplit the hi and lo halves.
 __device__ __forceinline__ v8h half_slab(v8i v, int h) {
     return __builtin_bit_cast(v8h, h == 0 ? __builtin_shufflevector(v, v, 0, 1, 2, 3)
                                           : __builtin_shufflevector(v, v, 4, 5, 6, 7));
@@ -184,48 +348,35 @@ __device__ __forceinline__ v4f multiply(v8h a, v8h b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-template <Mode kMode, bool kSplit, class T, int BM, int BN, int WAVES_M, int WAVES_N>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(ProdArgs a, int tiles_m, int tiles_n) {
+constexpr int kFinishRows = 4;   // rows of fragments that `finish` takes at a time: its LDS is 16 KB a wave
+
+template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 2) void ortho_product_kernel(ProdArgs a, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
-    constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
-    constexpr bool kSymmetric = kMode != kStep;
-    __shared__ __align__(1024) uint8_t lds[2][(BM + BN) * kSlab];
+    constexpr int TM = BM / WAVES_M / 16, TN = BM / WAVES_N / 16;
+    constexpr int TF = TM < kFinishRows ? TM : kFinishRows;
+    constexpr int kStageBytes = 2 * BM * kSlab;
+    constexpr int kFinishBytes = TF * 16 * TN * 16 * 4;
+    static_assert(kWaves * kFinishBytes <= kStages * kStageBytes, "every wave's results fit in LDS");
+    __shared__ __align__(1024) uint8_t lds[kStages * kStageBytes];
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int r16 = lane & 15, g = lane >> 4;
-    int bm, bn;
+    const int tiles = gridDim.x / a.parts;
     const int id = xcd_order(blockIdx.x, gridDim.x);
-    if constexpr (kSymmetric) {   // the tiles on and below the diagonal, row by row
-        bm = (int)((sqrtf(8.0f * (float)id + 1.0f) - 1.0f) * 0.5f);
-        while (bm * (bm + 1) / 2 > id) --bm;
-        while ((bm + 1) * (bm + 2) / 2 <= id) ++bm;
-        bn = id - bm * (bm + 1) / 2;
-    } else {
-        banded_tile(id, tiles_m, tiles_n, 8, bm, bn);
-    }
-    const int m0 = bm * BM, n0 = bn * BN;
+    const int part = id / tiles, tile = id - part * tiles;
+    const TilePlace at = tile_place<kMode>(tile, tiles_m, tiles_n);
+    const int m0 = at.bm * BM, n0 = at.bn * BM;
     const int64_t item = blockIdx.z;
-    const uint32_t ld = (uint32_t)a.k * 2;
-    const int per = a.k / 64;
-    const int slabs = kSplit ? 3 * per : per;
-    const uint8_t* p_hi = (const uint8_t*)(a.p_hi + item * a.p_batch + (int64_t)m0 * a.k);
-    const uint8_t* q_hi = (const uint8_t*)(a.q_hi + item * a.q_batch + (int64_t)n0 * a.k);
-    const uint8_t* p_lo = kSplit ? (const uint8_t*)(a.p_lo + item * a.p_batch + (int64_t)m0 * a.k) : nullptr;
-    const uint8_t* q_lo = kSplit ? (const uint8_t*)(a.q_lo + item * a.q_batch + (int64_t)n0 * a.k) : nullptr;
+    const uint32_t ld = (uint32_t)a.k * Halves2<kSplit>::kPer * 2;
+    const int slabs = a.k / Halves2<kSplit>::kSlabCols;
+    const int first = (int)((int64_t)slabs * part / a.parts), last = (int)((int64_t)slabs * (part + 1) / a.parts);
 
-    SlabSource<BM, kWaves> src_p;
-    SlabSource<BN, kWaves> src_q;
-    src_p.set(p_hi, ld, a.rows - m0, wave, lane);
-    src_q.set(q_hi, ld, a.cols - n0, wave, lane);
-    auto fetch = [&](int s, uint8_t* to) {
-        const int part = kSplit ? s / per : 0;   // hi hi, hi lo, lo hi
-        const uint32_t at = (uint32_t)(s - part * per) * kSlab;
-        src_p.base = kSplit && part == 2 ? p_lo : p_hi;
-        src_q.base = kSplit && part == 1 ? q_lo : q_hi;
-        src_p.fetch(at, to, wave);
-        src_q.fetch(at, to + BM * kSlab, wave);
-    };
+    using Source = SlabSource<BM, kWaves>;
+    Source src_p, src_q;
+    src_p.set((const uint8_t*)(a.p + item * a.p_batch) + (int64_t)m0 * ld, ld, a.rows - m0, wave, lane);
+    src_q.set((const uint8_t*)(a.q + item * a.q_batch) + (int64_t)n0 * ld, ld, a.cols - n0, wave, lane);
 
     v4f acc[TM][TN];
 #pragma unroll
@@ -234,148 +385,183 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void ortho_product_kernel(P
         for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
 
-    fetch(0, lds[0]);
-    for (int s = 0; s < slabs; ++s) {
-        wait_loads();
-        __syncthreads();   // slab s is in LDS, and nobody reads the other buffer any more
-        if (s + 1 < slabs) fetch(s + 1, lds[(s + 1) & 1]);
-        const uint8_t* lp = lds[s & 1];
-        const uint8_t* lq = lp + BM * kSlab;
-        v8i fq[TN];
+    pipelined<kStages, 2 * Source::kLoads>(
+        last - first,
+        [&](int s, int slot) {
+            uint8_t* stage = lds + slot * kStageBytes;
+            src_p.fetch((uint32_t)(first + s) * kSlab, stage, wave);
+            src_q.fetch((uint32_t)(first + s) * kSlab, stage + BM * kSlab, wave);
+        },
+        [&](int slot) {
+            const uint8_t* lp = lds + slot * kStageBytes;
+            const uint8_t* lq = lp + BM * kSlab;
+            v8i fq[TN], fp[2];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fq[j] = read_slab(lq, wn0 + j * 16 + r16, g);
+            for (int j = 0; j < TN; ++j) fq[j] = read_slab(lq, wn0 + j * 16 + r16, g);
+            fp[0] = read_slab(lp, wm0 + r16, g);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const v8i fp = read_slab(lp, wm0 + i * 16 + r16, g);
+            for (int i = 0; i < TM; ++i) {
+                if (i + 1 < TM) fp[(i + 1) & 1] = read_slab(lp, wm0 + (i + 1) * 16 + r16, g);
+                const v8h p0 = half_slab(fp[i & 1], 0), p1 = half_slab(fp[i & 1], 1);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], 0), p0, acc[i][j]);
+                if constexpr (kSplit) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], h), half_slab(fp, h), acc[i][j]);
-        }
-    }
-
-    // A lane's four sums are neighbours along a row of the result.
-    const int64_t o = item * a.o_batch;
+                    for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], 0), p1, acc[i][j]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int row = m0 + wm0 + i * 16 + r16;
-        if (row >= a.rows) continue;
+                    for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], 1), p0, acc[i][j]);
+                } else {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int col = n0 + wn0 + j * 16 + g * 4;
-            if (col >= a.cols) continue;
-            const int64_t at = o + (int64_t)row * a.cols + col;
-            float v[4];
-            if constexpr (kMode == kGram) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = a.alpha * acc[i][j][e];
-            } else {
-                const v4h hi = *(const v4h*)((kMode == kPoly ? a.a_hi : a.o_hi) + at);
-                v4h lo = {0, 0, 0, 0};
-                if (kMode == kStep || kSplit) lo = *(const v4h*)((kMode == kPoly ? a.a_lo : a.o_lo) + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = fmaf(a.alpha, (float)hi[e] + (float)lo[e], a.beta * acc[i][j][e]);
-            }
-            if (kMode == kStep && a.out) {
-                T* out = (T*)a.out + item * a.out_batch;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (row < a.m && col + e < a.n)
-                        out[a.tall ? (int64_t)(col + e) * a.m + row : (int64_t)row * a.n + col + e] =
-                            from_f32<T>(v[e] * (1.0f / kXScale));
-                continue;
-            }
-            v4h hi, lo;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                _Float16 h, l;
-                split(v[e], h, l);
-                hi[e] = h;
-                lo[e] = l;
-            }
-            *(v4h*)(a.o_hi + at) = hi;
-            if (kMode == kStep || kSplit) *(v4h*)(a.o_lo + at) = lo;
-            if (kMode == kStep || bm != bn) {   // the mirror image, or the transpose
-                _Float16* t_hi = (kMode == kStep ? a.t_hi : a.o_hi) + o + (int64_t)col * a.rows + row;
-                _Float16* t_lo = kSplit ? (kMode == kStep ? a.t_lo : a.o_lo) + o + (int64_t)col * a.rows + row : nullptr;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t_hi[(int64_t)e * a.rows] = hi[e];
-                    if (kSplit) t_lo[(int64_t)e * a.rows] = lo[e];
+                    for (int j = 0; j < TN; ++j) acc[i][j] = multiply(half_slab(fq[j], 1), p1, acc[i][j]);
                 }
+                if (i + 1 < TM) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x8, (kSplit ? 3 : 2) * TN, 0);
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
+        });
+
+    if (a.parts > 1) {
+        const int64_t block = ((item * a.parts + part) * tiles + tile) * kWaves + wave;
+        v4f* to = (v4f*)a.partial + block * (TM * TN * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) to[(i * TN + j) * 64] = acc[i][j];
+        return;
+    }
+    meet();   // nobody reads the operands any more
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += TF) {
+        v4f some[TF][TN];
+#pragma unroll
+        for (int i = 0; i < TF; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) some[i][j] = acc[i0 + i][j];
+        __builtin_amdgcn_sched_barrier(0);
+        finish<kMode, kSplit, T, TF, TN>(a, some, m0 + wm0 + i0 * 16, n0 + wn0, item, kMode == kStep || at.bm != at.bn,
+                                         lds + wave * kFinishBytes, lane);
     }
 }
 
+// The parts' sums, added in their order, and the result from them: one wave for each kFinishRows rows of fragments.
 template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N>
-void launch_tiles(const ProdArgs& a, int64_t batch, hipStream_t st) {
+__global__ __launch_bounds__(64) void ortho_join_kernel(ProdArgs a, int tiles_m, int tiles_n) {
+    constexpr int kWaves = WAVES_M * WAVES_N;
+    constexpr int TM = BM / WAVES_M / 16, TN = BM / WAVES_N / 16;
+    constexpr int TF = TM < kFinishRows ? TM : kFinishRows, kPieces = TM / TF;
+    __shared__ __align__(1024) uint8_t lds[TF * 16 * TN * 16 * 4];
+    const int lane = threadIdx.x;
+    const int tiles = gridDim.x / (kWaves * kPieces);
+    const int piece = blockIdx.x % kPieces, wave = blockIdx.x / kPieces % kWaves, tile = blockIdx.x / (kPieces * kWaves);
+    const int64_t item = blockIdx.z;
+    const TilePlace at = tile_place<kMode>(tile, tiles_m, tiles_n);
+    const int row0 = at.bm * BM + (wave / WAVES_N) * TM * 16 + piece * TF * 16;
+    const int col0 = at.bn * BM + (wave % WAVES_N) * TN * 16;
+    v4f acc[TF][TN];
+    for (int part = 0; part < a.parts; ++part) {
+        const int64_t block = ((item * a.parts + part) * tiles + tile) * kWaves + wave;
+        const v4f* from = (const v4f*)a.partial + block * (TM * TN * 64) + piece * (TF * TN * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < TF; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const v4f v = from[(i * TN + j) * 64];
+                acc[i][j] = part ? acc[i][j] + v : v;
+            }
+    }
+    finish<kMode, kSplit, T, TF, TN>(a, acc, row0, col0, item, kMode == kStep || at.bm != at.bn, lds, lane);
+}
+
+template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages>
+void launch_tiles(ProdArgs a, int64_t batch, int parts, hipStream_t st) {
     const int tm = (a.rows + BM - 1) / BM, tn = (a.cols + BM - 1) / BM;
     const unsigned tiles = kMode == kStep ? (unsigned)tm * tn : (unsigned)tm * (tm + 1) / 2;
-    ortho_product_kernel<kMode, kSplit, T, BM, BM, WAVES_M, WAVES_N>
-        <<<dim3(tiles, 1, (unsigned)batch), 64 * WAVES_M * WAVES_N, 0, st>>>(a, tm, tn);
+    a.parts = parts;
+    ortho_product_kernel<kMode, kSplit, T, BM, WAVES_M, WAVES_N, kStages>
+        <<<dim3(tiles * parts, 1, (unsigned)batch), 64 * WAVES_M * WAVES_N, 0, st>>>(a, tm, tn);
+    if (parts > 1) {
+        constexpr int kPieces = BM / WAVES_M / 16 / kFinishRows;
+        ortho_join_kernel<kMode, kSplit, T, BM, WAVES_M, WAVES_N>
+            <<<dim3(tiles * WAVES_M * WAVES_N * kPieces, 1, (unsigned)batch), 64, 0, st>>>(a, tm, tn);
+    }
+}
+
+// How a symmetric product of `rows` over k is cut: tiles of 256 (in `parts` parts of the k loop where they leave most
+// of the card idle), of 128 or of 64.
+struct Cut {
+    int tile, parts;
+};
+
+inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, bool symmetric, int slab_cols) {
+    const auto tiles = [&](int64_t size) {
+        const int64_t tm = (rows + size - 1) / size, tn = (cols + size - 1) / size;
+        return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
+    };
+    constexpr int64_t kCus = 256;
+    const int64_t slabs = k / slab_cols;
+    if (tiles(256) >= kCus * 3 / 4) return {256, 1};
+    if (symmetric && tiles(256) >= 24) {
+        const int64_t parts = std::min(kCus / tiles(256), slabs / 8);
+        if (parts > 1) return {256, (int)parts};
+    }
+    if (tiles(128) >= kCus * 3 / 4) return {128, 1};
+    return {64, 1};
 }
 
 template <Mode kMode, bool kSplit, class T>
 void launch_product(const ProdArgs& a, int64_t batch, hipStream_t st) {
-    const auto tiles = [&](int64_t size) {
-        const int64_t tm = (a.rows + size - 1) / size, tn = (a.cols + size - 1) / size;
-        return batch * (kMode == kStep ? tm * tn : tm * (tm + 1) / 2);
-    };
-    if (tiles(256) >= 192)
-        launch_tiles<kMode, kSplit, T, 256, 2, 4>(a, batch, st);
-    else if (tiles(128) >= 192)
-        launch_tiles<kMode, kSplit, T, 128, 2, 2>(a, batch, st);
+    const Cut c = cut_product(batch, a.rows, a.cols, a.k, kMode != kStep, Halves2<kSplit>::kSlabCols);
+    if (c.tile == 256)
+        launch_tiles<kMode, kSplit, T, 256, 2, 4, 2>(a, batch, c.parts, st);
+    else if (c.tile == 128)
+        launch_tiles<kMode, kSplit, T, 128, 2, 2, 2>(a, batch, 1, st);
     else
-        launch_tiles<kMode, kSplit, T, 64, 2, 2>(a, batch, st);
+        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4>(a, batch, 1, st);
 }
 
 template <bool kSplit, class Out>
 hipError_t iterate(const OrthoArgs& o, const Layout& l, hipStream_t st) {
     unsigned char* ws = o.ws;
     auto at = [&](size_t off) { return (_Float16*)(ws + off); };
-    const int64_t x_batch = l.mp * l.np, s_batch = l.mp * l.mp;
+    constexpr int64_t kPer = Halves2<kSplit>::kPer;
+    const int64_t x_batch = l.mp * l.np * kPer, s_batch = l.mp * l.mp * kPer;
     for (int s = 0; s < o.steps; ++s) {
         const int cur = s & 1, next = cur ^ 1;
         ProdArgs gram{};
-        gram.p_hi = gram.q_hi = at(l.x_hi);
-        gram.p_lo = gram.q_lo = at(l.x_lo);
+        gram.p = gram.q = at(l.x);
         gram.p_batch = gram.q_batch = x_batch;
         gram.rows = gram.cols = (int32_t)l.mp;
         gram.k = (int32_t)l.np;
-        gram.o_hi = at(l.a_hi);
-        gram.o_lo = at(l.a_lo);
+        gram.o = gram.t = at(l.a);
         gram.o_batch = s_batch;
         gram.alpha = kAScale / (kXScale * kXScale);
+        gram.partial = (float*)(ws + l.sums);
         launch_product<kGram, kSplit, float>(gram, o.batch, st);
 
         ProdArgs poly{};
-        poly.p_hi = poly.q_hi = poly.a_hi = at(l.a_hi);
-        poly.p_lo = poly.q_lo = poly.a_lo = at(l.a_lo);
+        poly.p = poly.q = poly.old = at(l.a);
         poly.p_batch = poly.q_batch = s_batch;
         poly.rows = poly.cols = poly.k = (int32_t)l.mp;
-        poly.o_hi = at(l.b_hi);
-        poly.o_lo = at(l.b_lo);
+        poly.o = poly.t = at(l.b);
         poly.o_batch = s_batch;
         poly.alpha = o.b;
         poly.beta = o.c / kAScale;
+        poly.partial = (float*)(ws + l.sums);
         launch_product<kPoly, kSplit, float>(poly, o.batch, st);
 
         ProdArgs step{};
-        step.p_hi = at(l.b_hi);
-        step.p_lo = at(l.b_lo);
+        step.p = at(l.b);
         step.p_batch = s_batch;
-        step.q_hi = at(l.xt_hi[cur]);
-        step.q_lo = at(l.xt_lo[cur]);
+        step.q = at(l.xt[cur]);
         step.q_batch = x_batch;
         step.rows = (int32_t)l.mp;
         step.cols = (int32_t)l.np;
         step.k = (int32_t)l.mp;
-        step.o_hi = at(l.x_hi);
-        step.o_lo = at(l.x_lo);
-        step.t_hi = at(l.xt_hi[next]);
-        step.t_lo = at(l.xt_lo[next]);
+        step.old = step.o = at(l.x);
+        step.old_lo = step.o_lo = at(l.x_lo);
+        step.lo_batch = l.mp * l.np;
+        step.t = at(l.xt[next]);
         step.o_batch = x_batch;
         step.alpha = o.a;
         step.beta = 1.0f / kAScale;
@@ -393,21 +579,66 @@ template <class In>
 hipError_t orthogonalize_from(const OrthoArgs& o, hipStream_t st) {
     const Layout l = make_layout(o.batch, o.rows, o.cols, o.out_type);
     double* partials = (double*)(o.ws + l.partials);
-    const int parts = (int)(o.rows < kPartials ? o.rows : kPartials);
-    square_sum_kernel<In><<<dim3((unsigned)parts, (unsigned)o.batch), 256, 0, st>>>((const In*)o.g, o.rows, o.cols,
-                                                                                   o.ld_g, o.batch_g, partials);
+    const int wide = (uintptr_t)o.g % 16 == 0 && o.ld_g * (int64_t)sizeof(In) % 16 == 0 &&
+                     (o.batch == 1 || o.batch_g * (int64_t)sizeof(In) % 16 == 0);
+    const int64_t chunks = o.rows * ((o.cols + 7) / 8);
+    const int parts = (int)std::min<int64_t>(kPartials, (chunks + 255) / 256);
+    square_sum_kernel<In><<<dim3((unsigned)parts, (unsigned)o.batch), 256, 0, st>>>(
+        (const In*)o.g, (int)o.rows, (int)o.cols, o.ld_g, o.batch_g, wide, partials);
     auto at = [&](size_t off) { return (_Float16*)(o.ws + off); };
-    _Float16 *x_hi = at(l.x_hi), *x_lo = at(l.x_lo), *xt_hi = at(l.xt_hi[0]);
-    _Float16* xt_lo = l.split ? at(l.xt_lo[0]) : nullptr;
     const int64_t rp = pad_up(o.rows), cp = pad_up(o.cols);
-    normalize_kernel<In><<<dim3((unsigned)(cp / 64), (unsigned)(rp / 64), (unsigned)o.batch), 256, 0, st>>>(
-        (const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, partials, parts, o.eps, l.tall ? xt_hi : x_hi,
-        l.tall ? xt_lo : x_lo, l.tall ? x_hi : xt_hi, l.tall ? x_lo : xt_lo, rp, cp);
+    const dim3 grid((unsigned)(cp / 64), (unsigned)(rp / 64), (unsigned)o.batch);
+    _Float16 *direct = at(l.tall ? l.xt[0] : l.x), *turned = at(l.tall ? l.x : l.xt[0]);
+    if (l.split)
+        normalize_kernel<In, true><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, wide,
+                                                         partials, parts, o.eps, direct, turned, nullptr, l.tall, rp, cp);
+    else
+        normalize_kernel<In, false><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, wide,
+                                                          partials, parts, o.eps, direct, turned, at(l.x_lo), l.tall, rp, cp);
     switch (o.out_type) {
         case BCJR_TYPE_F32: return iterate<true, float>(o, l, st);
         case BCJR_TYPE_BF16: return iterate<false, __hip_bfloat16>(o, l, st);
         default: return iterate<true, _Float16>(o, l, st);
     }
+}
+
+}  // namespace
+
+namespace {
+
+Layout make_layout(int64_t batch, int64_t rows, int64_t cols, int32_t out_type) {
+    Layout l{};
+    l.tall = rows > cols;
+    l.m = l.tall ? cols : rows;
+    l.n = l.tall ? rows : cols;
+    l.mp = pad_up(l.m);
+    l.np = pad_up(l.n);
+    l.split = out_type != BCJR_TYPE_BF16;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += area(bytes);
+        return here;
+    };
+    const size_t per = l.split ? 4 : 2;   // bytes of an element of a product's operand
+    const size_t x = (size_t)batch * l.mp * l.np, s = (size_t)batch * l.mp * l.mp;
+    l.partials = take((size_t)batch * kPartials * 8);
+    l.x = take(x * per);
+    l.x_lo = l.split ? l.x : take(x * 2);
+    l.xt[0] = take(x * per);
+    l.xt[1] = take(x * per);
+    l.a = take(s * per);
+    l.b = take(s * per);
+    size_t sums = 0;   // the symmetric products' partial sums
+    for (const int64_t k : {l.np, l.mp}) {
+        const Cut c = cut_product(batch, l.mp, l.mp, k, true, l.split ? 32 : 64);
+        const size_t tm = (size_t)((l.mp + c.tile - 1) / c.tile);
+        const size_t need = c.parts > 1 ? (size_t)batch * c.parts * (tm * (tm + 1) / 2) * c.tile * c.tile * 4 : 0;
+        sums = need > sums ? need : sums;
+    }
+    l.sums = take(sums);
+    l.total = at;
+    return l;
 }
 
 }  // namespace
