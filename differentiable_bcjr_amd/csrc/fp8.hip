@@ -270,9 +270,9 @@ __device__ __forceinline__ void take(v8i codes, Halves& out) { out = widen(codes
 
 // A stage of the k loop in LDS: the slabs of BM rows of a and BN rows of b, and the scales of those rows' blocks (b's
 // once for each row, also where a block is 128 rows).
-template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kWavesPerSimd, bool kRowScales>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, kWavesPerSimd) void product_kernel(ProductArgs a, int tiles_m,
-                                                                                        int tiles_n) {
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kGroups, bool kRowScales>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_kernel(ProductArgs a, int tiles_m,
+                                                                                      int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
     constexpr bool kWide = sizeof(T) == 4;
     constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
@@ -281,9 +281,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, kWavesPerSimd) void product
     static_assert(kScaleLoads <= kWaves, "one load of scales a wave");
     static_assert(kRowScales || 128 % (BN / WAVES_N) == 0, "a wave's columns lie in one block of b");
     using Frag = std::conditional_t<kWide, Halves, v8i>;
-    __shared__ __align__(1024) uint8_t lds[kStages * kStageBytes];
+    __shared__ __align__(1024) uint8_t all_lds[kGroups * kStages * kStageBytes];
     const int t = threadIdx.x, lane = t & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int any_wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int group = any_wave / kWaves, wave = any_wave % kWaves;
+    uint8_t* const lds = all_lds + group * (kStages * kStageBytes);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     int bm, bn;
     banded_tile(xcd_order(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8, bm, bn);
@@ -394,30 +396,38 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, kWavesPerSimd) void product
         }
     };
 
+    // group i takes the whole slabs i, i + kGroups, ..., the last group also the cut one
     const int full = a.k / kSlab, tail = a.k % kSlab;
+    const int mine = (full - group + kGroups - 1) / kGroups;
     pipelined<kStages, SourceA::kLoads + SourceB::kLoads + 1>(
-        full,
+        (full + kGroups - 1) / kGroups, mine,
         [&](int s, int slot) {
             uint8_t* stage = lds + slot * kStageBytes;
-            src_a.fetch((uint32_t)s * kSlab, stage, wave);
-            src_b.fetch((uint32_t)s * kSlab, stage + BM * kSlab, wave);
-            fetch_scales(s, stage);
+            const int slab = s * kGroups + group;
+            src_a.fetch((uint32_t)slab * kSlab, stage, wave);
+            src_b.fetch((uint32_t)slab * kSlab, stage + BM * kSlab, wave);
+            fetch_scales(slab, stage);
         },
         [&](int slot) { multiply(lds + slot * kStageBytes); });
     if (tail) {
         meet();
-        fetch_scales(full, lds);
-        fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, lds, wave, lane);
-        fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, lds + BM * kSlab, wave, lane);
-        wait_loads<0>();
+        if (group == kGroups - 1) {
+            fetch_scales(full, lds);
+            fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, lds, wave, lane);
+            fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, lds + BM * kSlab, wave, lane);
+            wait_loads<0>();
+        }
         meet();
-        multiply(lds);
+        if (group == kGroups - 1) multiply(lds);
     }
 
     using Tile = WaveTile<T, TM * 16, TN * 16>;
-    static_assert(kWaves * Tile::kBytes <= (int)sizeof(lds), "every wave's results fit in LDS");
+    constexpr int kJoinAt = kWaves * Tile::kBytes, kJoinBytes = (kGroups - 1) * kWaves * TM * TN * 1024;
+    static_assert(kJoinAt + kJoinBytes <= (int)sizeof(all_lds), "every wave's results and the groups' sums fit in LDS");
     meet();   // nobody reads the operands any more
-    uint8_t* mine = lds + wave * Tile::kBytes;
+    join_groups<kGroups, kWaves>(acc, group, wave, lane, all_lds + kJoinAt);
+    if (group > 0) return;
+    uint8_t* mine_lds = all_lds + wave * Tile::kBytes;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -425,11 +435,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, kWavesPerSimd) void product
             T e[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) e[x] = from_f32<T>(acc[i][j][x]);
-            Tile::put(mine, i * 16 + r16, j * 16 + g * 4, e);
+            Tile::put(mine_lds, i * 16 + r16, j * 16 + g * 4, e);
         }
     wave_fence();
     const bool wide = (uintptr_t)a.out % 16 == 0 && (a.ld_out * sizeof(T)) % 16 == 0;
-    Tile::store(mine, (T*)a.out + (int64_t)(m0 + wm0) * a.ld_out + n0 + wn0, a.ld_out, rows_a - wm0, rows_b - wn0, wide,
+    Tile::store(mine_lds, (T*)a.out + (int64_t)(m0 + wm0) * a.ld_out + n0 + wn0, a.ld_out, rows_a - wm0, rows_b - wn0, wide,
                 lane);
 }
 
@@ -559,19 +569,18 @@ void few_rows(const ProductArgs& a, hipStream_t st) {
         few_rows_kernel<T, X, false><<<grid, waves * 64, 0, st>>>(a, wide);
 }
 
-template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kWavesPerSimd, bool kRows = true>
+template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kGroups, bool kRows = true>
 void product_tiles(const ProductArgs& a, hipStream_t st) {
     const int tm = (a.m + BM - 1) / BM, tn = (a.n + BN - 1) / BN;
     const unsigned grid = (unsigned)tm * (unsigned)tn;
-    constexpr int kThreads = 64 * WAVES_M * WAVES_N;
+    constexpr int kThreads = 64 * WAVES_M * WAVES_N * kGroups;
     if constexpr (kRows) {
         if (a.b_rows == 1) {
-            product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kWavesPerSimd, true>
-                <<<grid, kThreads, 0, st>>>(a, tm, tn);
+            product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kGroups, true><<<grid, kThreads, 0, st>>>(a, tm, tn);
             return;
         }
     }
-    product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kWavesPerSimd, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
+    product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kGroups, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
 }
 
 template <class T>
@@ -580,13 +589,15 @@ hipError_t product(const ProductArgs& a, hipStream_t st) {
     if (a.m <= kFewRows) {
         few_rows<T, uint8_t>(a, st);
     } else if (sizeof(T) == 2 && a.b_rows == 128 && tiles(256, 256) >= 256) {
-        if constexpr (sizeof(T) == 2) product_tiles<T, 256, 256, 2, 4, 2, 2, false>(a, st);
+        if constexpr (sizeof(T) == 2) product_tiles<T, 256, 256, 2, 4, 2, 1, false>(a, st);
     } else if (tiles(256, 128) >= 256) {
-        product_tiles<T, 256, 128, 4, 2, 3, 2>(a, st);
+        product_tiles<T, 256, 128, 4, 2, 3, 1>(a, st);
     } else if (tiles(128, 128) >= 256) {
-        product_tiles<T, 128, 128, 2, 2, 2, 2>(a, st);
-    } else {
+        product_tiles<T, 128, 128, 2, 2, 2, 1>(a, st);
+    } else if (tiles(64, 64) <= 256 && a.k >= 8 * kSlab) {
         product_tiles<T, 64, 64, 2, 2, 4, 2>(a, st);
+    } else {
+        product_tiles<T, 64, 64, 2, 2, 4, 1>(a, st);
     }
     return hipGetLastError();
 }

@@ -56,12 +56,13 @@ __device__ __forceinline__ void meet() {
 // The k loop: stage s of `total` is loaded into LDS slot s mod kStages, kStages - 1 stages ahead of its use.  `issue`
 // issues kLoads loads in every wave and no others are in flight; `use` reads the slot.  One meeting a stage: behind it
 // the stage is there for all waves (each has waited for its own loads), and the slot that is loaded next is no longer
-// read (it was used in the step before).
+// read (it was used in the step before).  Waves that have fewer stages of their own (`mine`, at least one) load their
+// last one again, so that every wave's loads can be counted alike, and use each once.
 template <int kStages, int kLoads, class Issue, class Use>
-__device__ __forceinline__ void pipelined(int total, Issue issue, Use use) {
+__device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s)
-        if (s < total) issue(s, s);
+        if (s < total) issue(min(s, mine - 1), s);
     int slot = 0;
 #pragma unroll 1
     for (int s = 0; s < total; ++s) {
@@ -70,9 +71,34 @@ __device__ __forceinline__ void pipelined(int total, Issue issue, Use use) {
         else
             wait_loads<0>();
         meet();
-        if (s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-        use(slot);
+        if (s + kStages - 1 < total) issue(min(s + kStages - 1, mine - 1), slot == 0 ? kStages - 1 : slot - 1);
+        if (s < mine) use(slot);
         slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+}
+
+// Adds up the sums of kGroups groups of waves that each took a share of the k loop, in their order; the first group's
+// waves leave with the total.  `wave`: within the group; `at`: a part of LDS that is otherwise unused from here on.
+template <int kGroups, int kWaves, int TM, int TN>
+__device__ __forceinline__ void join_groups(v4f (&acc)[TM][TN], int group, int wave, int lane, uint8_t* at) {
+    if constexpr (kGroups > 1) {
+        if (group > 0) {
+            v4f* to = (v4f*)at + ((group - 1) * kWaves + wave) * (TM * TN * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) to[(i * TN + j) * 64] = acc[i][j];
+        }
+        meet();
+        if (group > 0) return;
+#pragma unroll
+        for (int other = 1; other < kGroups; ++other) {
+            const v4f* from = (const v4f*)at + ((other - 1) * kWaves + wave) * (TM * TN * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] += from[(i * TN + j) * 64];
+        }
     }
 }
 

@@ -350,17 +350,21 @@ __device__ __forceinline__ v4f multiply(v8h a, v8h b, v4f c) {
 
 constexpr int kFinishRows = 4;   // rows of fragments that `finish` takes at a time: its LDS is 16 KB a wave
 
-template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 2) void ortho_product_kernel(ProdArgs a, int tiles_m, int tiles_n) {
+template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages, int kGroups>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void ortho_product_kernel(ProdArgs a, int tiles_m,
+                                                                                            int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
     constexpr int TM = BM / WAVES_M / 16, TN = BM / WAVES_N / 16;
     constexpr int TF = TM < kFinishRows ? TM : kFinishRows;
     constexpr int kStageBytes = 2 * BM * kSlab;
     constexpr int kFinishBytes = TF * 16 * TN * 16 * 4;
-    static_assert(kWaves * kFinishBytes <= kStages * kStageBytes, "every wave's results fit in LDS");
-    __shared__ __align__(1024) uint8_t lds[kStages * kStageBytes];
+    constexpr int kJoinAt = kWaves * kFinishBytes, kJoinBytes = (kGroups - 1) * kWaves * TM * TN * 1024;
+    __shared__ __align__(1024) uint8_t all_lds[kGroups * kStages * kStageBytes];
+    static_assert(kJoinAt + kJoinBytes <= (int)sizeof(all_lds), "every wave's results and the groups' sums fit in LDS");
     const int t = threadIdx.x, lane = t & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int any_wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int group = any_wave / kWaves, wave = any_wave % kWaves;
+    uint8_t* const lds = all_lds + group * (kStages * kStageBytes);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int r16 = lane & 15, g = lane >> 4;
     const int tiles = gridDim.x / a.parts;
@@ -385,12 +389,14 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 2) void ortho_product_kerne
         for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
 
+    // group i takes slabs first + i, first + i + kGroups, ...
     pipelined<kStages, 2 * Source::kLoads>(
-        last - first,
+        (last - first + kGroups - 1) / kGroups, (last - first - group + kGroups - 1) / kGroups,
         [&](int s, int slot) {
             uint8_t* stage = lds + slot * kStageBytes;
-            src_p.fetch((uint32_t)(first + s) * kSlab, stage, wave);
-            src_q.fetch((uint32_t)(first + s) * kSlab, stage + BM * kSlab, wave);
+            const uint32_t at = (uint32_t)(first + s * kGroups + group) * kSlab;
+            src_p.fetch(at, stage, wave);
+            src_q.fetch(at, stage + BM * kSlab, wave);
         },
         [&](int slot) {
             const uint8_t* lp = lds + slot * kStageBytes;
@@ -431,6 +437,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 2) void ortho_product_kerne
         return;
     }
     meet();   // nobody reads the operands any more
+    join_groups<kGroups, kWaves>(acc, group, wave, lane, all_lds + kJoinAt);
+    if (group > 0) return;
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += TF) {
         v4f some[TF][TN];
@@ -440,16 +448,18 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, 2) void ortho_product_kerne
             for (int j = 0; j < TN; ++j) some[i][j] = acc[i0 + i][j];
         __builtin_amdgcn_sched_barrier(0);
         finish<kMode, kSplit, T, TF, TN>(a, some, m0 + wm0 + i0 * 16, n0 + wn0, item, kMode == kStep || at.bm != at.bn,
-                                         lds + wave * kFinishBytes, lane);
+                                         all_lds + wave * kFinishBytes, lane);
     }
 }
 
-// The parts' sums, added in their order, and the result from them: one wave for each kFinishRows rows of fragments.
+constexpr int kJoinRows = 2;
+
+// The parts' sums, added in their order, and the result from them: one wave for each kJoinRows rows of fragments.
 template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(64) void ortho_join_kernel(ProdArgs a, int tiles_m, int tiles_n) {
     constexpr int kWaves = WAVES_M * WAVES_N;
     constexpr int TM = BM / WAVES_M / 16, TN = BM / WAVES_N / 16;
-    constexpr int TF = TM < kFinishRows ? TM : kFinishRows, kPieces = TM / TF;
+    constexpr int TF = kJoinRows, kPieces = TM / TF;
     __shared__ __align__(1024) uint8_t lds[TF * 16 * TN * 16 * 4];
     const int lane = threadIdx.x;
     const int tiles = gridDim.x / (kWaves * kPieces);
@@ -459,6 +469,7 @@ __global__ __launch_bounds__(64) void ortho_join_kernel(ProdArgs a, int tiles_m,
     const int row0 = at.bm * BM + (wave / WAVES_N) * TM * 16 + piece * TF * 16;
     const int col0 = at.bn * BM + (wave % WAVES_N) * TN * 16;
     v4f acc[TF][TN];
+#pragma unroll 4
     for (int part = 0; part < a.parts; ++part) {
         const int64_t block = ((item * a.parts + part) * tiles + tile) * kWaves + wave;
         const v4f* from = (const v4f*)a.partial + block * (TM * TN * 64) + piece * (TF * TN * 64) + lane;
@@ -473,24 +484,24 @@ __global__ __launch_bounds__(64) void ortho_join_kernel(ProdArgs a, int tiles_m,
     finish<kMode, kSplit, T, TF, TN>(a, acc, row0, col0, item, kMode == kStep || at.bm != at.bn, lds, lane);
 }
 
-template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages>
+template <Mode kMode, bool kSplit, class T, int BM, int WAVES_M, int WAVES_N, int kStages, int kGroups>
 void launch_tiles(ProdArgs a, int64_t batch, int parts, hipStream_t st) {
     const int tm = (a.rows + BM - 1) / BM, tn = (a.cols + BM - 1) / BM;
     const unsigned tiles = kMode == kStep ? (unsigned)tm * tn : (unsigned)tm * (tm + 1) / 2;
     a.parts = parts;
-    ortho_product_kernel<kMode, kSplit, T, BM, WAVES_M, WAVES_N, kStages>
-        <<<dim3(tiles * parts, 1, (unsigned)batch), 64 * WAVES_M * WAVES_N, 0, st>>>(a, tm, tn);
+    ortho_product_kernel<kMode, kSplit, T, BM, WAVES_M, WAVES_N, kStages, kGroups>
+        <<<dim3(tiles * parts, 1, (unsigned)batch), 64 * WAVES_M * WAVES_N * kGroups, 0, st>>>(a, tm, tn);
     if (parts > 1) {
-        constexpr int kPieces = BM / WAVES_M / 16 / kFinishRows;
+        constexpr int kPieces = BM / WAVES_M / 16 / kJoinRows;
         ortho_join_kernel<kMode, kSplit, T, BM, WAVES_M, WAVES_N>
             <<<dim3(tiles * WAVES_M * WAVES_N * kPieces, 1, (unsigned)batch), 64, 0, st>>>(a, tm, tn);
     }
 }
 
-// How a symmetric product of `rows` over k is cut: tiles of 256 (in `parts` parts of the k loop where they leave most
-// of the card idle), of 128 or of 64.
+// How a product over k is cut: tiles of 256 (a symmetric product's in `parts` parts of the k loop where they leave most
+// of the card idle), of 128 or of 64, the k loop of a tile shared by `groups` groups of waves.
 struct Cut {
-    int tile, parts;
+    int tile, parts, groups;
 };
 
 inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, bool symmetric, int slab_cols) {
@@ -500,24 +511,29 @@ inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, boo
     };
     constexpr int64_t kCus = 256;
     const int64_t slabs = k / slab_cols;
-    if (tiles(256) >= kCus * 3 / 4) return {256, 1};
+    if (tiles(256) >= kCus * 3 / 4) return {256, 1, 1};
     if (symmetric && tiles(256) >= 24) {
         const int64_t parts = std::min(kCus / tiles(256), slabs / 8);
-        if (parts > 1) return {256, (int)parts};
+        if (parts > 1) return {256, (int)parts, 1};
     }
-    if (tiles(128) >= kCus * 3 / 4) return {128, 1};
-    return {64, 1};
+    if (tiles(128) > kCus) return {128, 1, 1};
+    if (tiles(128) >= kCus * 3 / 4) return {128, 1, 2};
+    return {64, 1, tiles(64) <= kCus && slabs >= 4 ? 2 : 1};
 }
 
 template <Mode kMode, bool kSplit, class T>
 void launch_product(const ProdArgs& a, int64_t batch, hipStream_t st) {
     const Cut c = cut_product(batch, a.rows, a.cols, a.k, kMode != kStep, Halves2<kSplit>::kSlabCols);
     if (c.tile == 256)
-        launch_tiles<kMode, kSplit, T, 256, 2, 4, 2>(a, batch, c.parts, st);
+        launch_tiles<kMode, kSplit, T, 256, 2, 4, 2, 1>(a, batch, c.parts, st);
+    else if (c.tile == 128 && c.groups == 1)
+        launch_tiles<kMode, kSplit, T, 128, 2, 2, 2, 1>(a, batch, 1, st);
     else if (c.tile == 128)
-        launch_tiles<kMode, kSplit, T, 128, 2, 2, 2>(a, batch, 1, st);
+        launch_tiles<kMode, kSplit, T, 128, 2, 2, 2, 2>(a, batch, 1, st);
+    else if (c.groups == 2)
+        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4, 2>(a, batch, 1, st);
     else
-        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4>(a, batch, 1, st);
+        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4, 1>(a, batch, 1, st);
 }
 
 template <bool kSplit, class Out>
