@@ -24,10 +24,11 @@ constexpr float kMinScale = 1.17549435e-38f;
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-__device__ __forceinline__ uint32_t max8(const float (&v)[8]) {
+template <class T>
+__device__ __forceinline__ uint32_t max8(const Eight<T>& v) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v.at(j)));
     return m;
 }
 
@@ -43,8 +44,10 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float r) {
-    return make_uint2(codes4(v[0] * r, v[1] * r, v[2] * r, v[3] * r), codes4(v[4] * r, v[5] * r, v[6] * r, v[7] * r));
+template <class T>
+__device__ __forceinline__ uint2 codes8(const Eight<T>& v, float r) {
+    return make_uint2(codes4(v.at(0) * r, v.at(1) * r, v.at(2) * r, v.at(3) * r),
+                      codes4(v.at(4) * r, v.at(5) * r, v.at(6) * r, v.at(7) * r));
 }
 
 __device__ __forceinline__ void store8(uint8_t* p, int count, uint2 w) {
@@ -59,19 +62,16 @@ __device__ __forceinline__ void store8(uint8_t* p, int count, uint2 w) {
 constexpr int kRowsPerGroup = 16;
 
 template <class T>
-__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int col_blocks, int wide) {
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int col_blocks) {
     const int t = threadIdx.x;
     const int cb = blockIdx.x % col_blocks;
     const int64_t row = (int64_t)(blockIdx.x / col_blocks) * kRowsPerGroup + (t >> 4);
     const int64_t col = (int64_t)cb * 128 + (t & 15) * 8;
     const bool have = row < a.rows;
     const int64_t left = have ? a.cols - col : 0;
-    float v[8] = {};
-    if (left > 0) load8((const T*)a.x + row * a.ld_x + col, (int)min(left, (int64_t)8), wide && left >= 8, v);
-    uint32_t m = max8(v);
-#pragma unroll
-    for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-    const float s = block_scale(m);
+    Eight<T> v;
+    v.load((const T*)a.x + row * a.ld_x + col, left);
+    const float s = block_scale(max16(max8(v)));
     if (left > 0) store8(a.q + row * a.ld_q + col, (int)min(left, (int64_t)8), codes8(v, 1.0f / s));
     if (have && (t & 15) == 0) a.scale[(int64_t)cb * a.rows + row] = s;
 }
@@ -80,8 +80,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int 
 // columns of eight consecutive rows, so both orientations leave it as words of eight codes; the transposed codes pass
 // through LDS to be written in whole 128-byte lines.
 template <class T, bool kSquare, bool kTransposed>
-__global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int col_blocks, int row_blocks,
-                                                            int wide) {
+__global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int col_blocks, int row_blocks) {
     __shared__ uint32_t col_max[4][128];
     __shared__ __align__(16) uint8_t codes_t[kTransposed ? 128 * 128 : 16];
     const int t = threadIdx.x;
@@ -91,22 +90,19 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int 
     const int64_t col = col0 + i * 8;
     const int64_t rows_left = a.rows - (row0 + band * 8);
     const int64_t cols_left = a.cols - col;
-    float v[8][8] = {};
-    if (cols_left > 0) {
+    Eight<T> v[8];
 #pragma unroll
-        for (int p = 0; p < 8; ++p)
-            if (p < rows_left)
-                load8((const T*)a.x + (row0 + band * 8 + p) * a.ld_x + col, (int)min(cols_left, (int64_t)8),
-                      wide && cols_left >= 8, v[p]);
-    }
+    for (int p = 0; p < 8; ++p)
+        v[p].load((const T*)a.x + (row0 + band * 8 + p) * a.ld_x + col, p < rows_left ? cols_left : 0);
 
     float inv_square = 0.0f;
     if constexpr (kSquare) {
         uint32_t m = 0;
 #pragma unroll
         for (int p = 0; p < 8; ++p) m = max(m, max8(v[p]));
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+        m = max16(m);
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
         if ((t & 63) == 0) col_max[t >> 6][0] = m;
         __syncthreads();
         m = max(max(col_max[0][0], col_max[1][0]), max(col_max[2][0], col_max[3][0]));
@@ -122,10 +118,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int 
     for (int p = 0; p < 8; ++p) {
         float r = inv_square;
         if constexpr (!kSquare) {
-            uint32_t m = max8(v[p]);
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-            const float s = block_scale(m);
+            const float s = block_scale(max16(max8(v[p])));
             r = 1.0f / s;
             if (i == 0 && p < rows_left) a.scale[(int64_t)cb * a.rows + row0 + band * 8 + p] = s;
         }
@@ -144,7 +137,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int 
             for (int j = 0; j < 8; ++j) {
                 m[j] = 0;
 #pragma unroll
-                for (int p = 0; p < 8; ++p) m[j] = max(m[j], abs_bits(v[p][j]));
+                for (int p = 0; p < 8; ++p) m[j] = max(m[j], abs_bits(v[p].at(j)));
                 m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 16));
                 m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], 32));
             }
@@ -166,8 +159,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int 
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float r = inv[j];
-            const uint2 w = make_uint2(codes4(v[0][j] * r, v[1][j] * r, v[2][j] * r, v[3][j] * r),
-                                       codes4(v[4][j] * r, v[5][j] * r, v[6][j] * r, v[7][j] * r));
+            const uint2 w = make_uint2(codes4(v[0].at(j) * r, v[1].at(j) * r, v[2].at(j) * r, v[3].at(j) * r),
+                                       codes4(v[4].at(j) * r, v[5].at(j) * r, v[6].at(j) * r, v[7].at(j) * r));
             *(uint2*)(codes_t + (i * 8 + j) * 128 + ((band ^ i) * 8)) = w;
         }
         __syncthreads();
@@ -193,19 +186,18 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int 
 
 template <class T>
 hipError_t quantize(const QuantizeArgs& a, hipStream_t st) {
-    const int wide = ((uintptr_t)a.x % 16 == 0 && (a.ld_x * sizeof(T)) % 16 == 0) ? 1 : 0;
     const int cb = (int)((a.cols + 127) / 128), rb = (int)((a.rows + 127) / 128);
     if (a.block_rows == 1 && !a.q_t) {
         const unsigned grid = (unsigned)cb * (unsigned)((a.rows + kRowsPerGroup - 1) / kRowsPerGroup);
-        quantize_rows_kernel<T><<<grid, 256, 0, st>>>(a, cb, wide);
+        quantize_rows_kernel<T><<<grid, 256, 0, st>>>(a, cb);
     } else {
         const unsigned grid = (unsigned)cb * (unsigned)rb;
         if (a.block_rows == 1)
-            quantize_tile_kernel<T, false, true><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+            quantize_tile_kernel<T, false, true><<<grid, 256, 0, st>>>(a, cb, rb);
         else if (a.q_t)
-            quantize_tile_kernel<T, true, true><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+            quantize_tile_kernel<T, true, true><<<grid, 256, 0, st>>>(a, cb, rb);
         else
-            quantize_tile_kernel<T, true, false><<<grid, 256, 0, st>>>(a, cb, rb, wide);
+            quantize_tile_kernel<T, true, false><<<grid, 256, 0, st>>>(a, cb, rb);
     }
     return hipGetLastError();
 }
@@ -445,109 +437,139 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
 
 // ---- few rows
 //
-// With at most 16 rows of a the product is bound by reading b, once.  A wave takes 16 rows of b straight from memory
-// into the MFMA's operand (lane l: the 16-byte chunks l >> 4 and (l >> 4) + 4 of row l & 15, so one load covers whole
-// 64-byte sectors), the workgroup's waves share the slabs of those rows among them, four slabs of each in flight, and
-// their sums meet in LDS in a fixed order.  a either comes as codes or as numbers that are quantized in the operand's
-// registers: the four lanes of a row hold its whole block, so its largest entry is two lane exchanges away.
+// With few rows of a the product is bound by reading b, once, and by latency.  A wave takes 16 rows of b straight from
+// memory into the MFMA's operand (lane l: the 16-byte chunks l >> 4 and (l >> 4) + 4 of row l & 15, so one load covers
+// whole 64-byte sectors), the workgroup's waves share the slabs of those rows among them, and their sums meet in LDS in
+// a fixed order.  All loads of the slabs that a wave takes at a time are issued before the first is used.  a (up to 16
+// rows for each of kTiles fragments) comes as codes; or, where it is small, as numbers, which every workgroup quantizes
+// into its LDS while its first rows of b are on their way.
 
 __device__ __forceinline__ v8i load_slab(const uint8_t* row, int at, int g, int k) {
     return __builtin_shufflevector(load_chunk(row, at + g * 16, k), load_chunk(row, at + 64 + g * 16, k), 0, 1, 2, 3, 4,
                                    5, 6, 7);
 }
 
-// The same chunks of a row of numbers, as codes; `scale` is the block's.
-template <class X>
-__device__ __forceinline__ v8i quantize_slab(const X* row, int at, int g, int k, bool have, bool wide, float& scale) {
-    float v[4][8];
-    uint32_t m = 0;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const int from = at + (h >> 1) * 64 + g * 16 + (h & 1) * 8;
-        const int left = have ? k - from : 0;
-        if (left > 0) {
-            load8(row + from, min(left, 8), wide && left >= 8, v[h]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
-        }
-        m = max(m, max8(v[h]));
-    }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    scale = block_scale(m);
-    const float r = 1.0f / scale;
-    v8i out;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        const uint2 c = codes8(v[h], r);
-        out[h * 2] = (int)c.x;
-        out[h * 2 + 1] = (int)c.y;
-    }
-    return out;
+// A whole slab's chunks.
+__device__ __forceinline__ v8i load_full_slab(const uint8_t* row, int at, int g) {
+    const v4i lo = *(const v4i*)(row + at + g * 16), hi = *(const v4i*)(row + at + 64 + g * 16);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-constexpr int kFewRows = 16;
-constexpr int kAhead = 4;   // slabs whose loads a wave has in flight
+constexpr int kFewRows = 4;          // rows that are quantized on the way,
+constexpr int kFewNumbers = 32768;   // and numbers, rows rounded up to whole blocks
+constexpr int kFewCodedRows = 32;    // rows of codes
 
 // X: the type of a's numbers, or uint8_t for codes.
-template <class T, class X, bool kRowScales>
-__global__ __launch_bounds__(1024) void few_rows_kernel(ProductArgs a, int wide) {
+template <class T, class X, int kTiles, bool kRowScales>
+__global__ __launch_bounds__(1024) void few_rows_kernel(ProductArgs a) {
     constexpr bool kWide = sizeof(T) == 4, kCodes = sizeof(X) == 1;
-    __shared__ float sums[16][256];
+    constexpr int kAhead = kTiles == 1 ? 4 : 2;   // slabs a wave takes at a time
+    using Frag = std::conditional_t<kWide, Halves, v8i>;
+    __shared__ float sums[16][256 * kTiles];
+    __shared__ __align__(16) uint8_t own_codes[kCodes ? 16 : kFewNumbers];   // [row][slab]
+    __shared__ float own_scales[kCodes ? 1 : kFewNumbers / kSlab];
     const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * 16;
-    const int slabs = (a.k + kSlab - 1) / kSlab;
+    const int full = a.k / kSlab, tail = a.k % kSlab, slabs = full + (tail ? 1 : 0);
     const uint8_t* b_row = a.b + (int64_t)min(n0 + r16, a.n - 1) * a.ld_b;
-    const bool have = r16 < a.m;
-    const X* a_row = (const X*)a.a + (int64_t)(have ? r16 : 0) * a.ld_a;
+    int row[kTiles];   // rows behind the last repeat it; their results are not stored
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) row[i] = min(i * 16 + r16, a.m - 1);
     const int sb_len = kRowScales ? a.n : (a.n + 127) / 128;
+    int sb_at[kRowScales ? 4 : 1];
+#pragma unroll
+    for (int e = 0; e < (kRowScales ? 4 : 1); ++e) sb_at[e] = kRowScales ? min(n0 + g * 4 + e, a.n - 1) : n0 / 128;
 
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s0 = wave; s0 < slabs; s0 += waves * kAhead) {
-        v8i fb[kAhead];
+    v4f acc[kTiles];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int s = s0 + u * waves;
-            if (s < slabs) fb[u] = load_slab(b_row, s * kSlab, g, a.k);
+    for (int i = 0; i < kTiles; ++i) acc[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+    struct Slab {
+        v8i b, a[kCodes ? kTiles : 1];
+        float sb[kRowScales ? 4 : 1], sa[kCodes ? kTiles : 1];
+    };
+    auto fetch = [&](int s, Slab& slab, auto whole) {
+        constexpr bool kFull = decltype(whole)::value;
+        slab.b = kFull ? load_full_slab(b_row, s * kSlab, g) : load_slab(b_row, s * kSlab, g, a.k);
+#pragma unroll
+        for (int e = 0; e < (kRowScales ? 4 : 1); ++e) slab.sb[e] = a.b_scale[(int64_t)s * sb_len + sb_at[e]];
+        if constexpr (kCodes) {
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const uint8_t* a_row = a.a + (int64_t)row[i] * a.ld_a;
+                slab.a[i] = kFull ? load_full_slab(a_row, s * kSlab, g) : load_slab(a_row, s * kSlab, g, a.k);
+                slab.sa[i] = a.a_scale[(int64_t)s * a.m + row[i]];
+            }
         }
+    };
+    auto use = [&](int s, const Slab& slab) {
+        Frag fb[1];
+        take(slab.b, fb[0]);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int s = s0 + u * waves;
-            if (s >= slabs) break;
-            float sa = 0.0f;
-            v8i fa;
+        for (int i = 0; i < kTiles; ++i) {
+            float sa;
+            Frag fa;
             if constexpr (kCodes) {
-                fa = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-                if (have) {
-                    fa = load_slab(a_row, s * kSlab, g, a.k);
-                    sa = a.a_scale[(int64_t)s * a.m + r16];
-                }
+                sa = slab.sa[i];
+                take(slab.a[i], fa);
             } else {
-                fa = quantize_slab(a_row, s * kSlab, g, a.k, have, wide != 0, sa);
+                sa = own_scales[row[i] * slabs + s];
+                take(load_full_slab(own_codes, (row[i] * slabs + s) * kSlab, g), fa);
             }
-            std::conditional_t<kWide, Halves, v8i> wa, wb[1];
-            take(fa, wa);
-            take(fb[u], wb[0]);
-            v4f sums4[1];
-            block_products(wb, wa, sums4);
-            const v4f p = sums4[0];
-            const float* sb = a.b_scale + (int64_t)s * sb_len;
-            if constexpr (kRowScales) {
+            v4f p[1];
+            block_products(fb, fa, p);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e] * sb[min(n0 + g * 4 + e, a.n - 1)], sa, acc[e]);
-            } else {
-                const float both = sa * sb[n0 / 128];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], both, acc[e]);
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kRowScales)
+                    acc[i][e] = fmaf(p[0][e] * slab.sb[e], sa, acc[i][e]);
+                else
+                    acc[i][e] = fmaf(p[0][e], sa * slab.sb[0], acc[i][e]);
             }
         }
+    };
+
+    // Slab s belongs to wave s mod waves: kAhead at a time, then one at a time, then the cut one.
+    Slab some[kAhead];
+    int s = wave;
+    bool ahead = s + (kAhead - 1) * waves < full;
+    auto fetch_some = [&] {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) fetch(s + u * waves, some[u], std::true_type{});
+        __builtin_amdgcn_sched_barrier(0);   // all of the loads, then their uses
+    };
+    if (ahead) fetch_some();
+    if constexpr (!kCodes) {   // 16 lanes a block, as in quantize_rows_kernel
+        for (int i = threadIdx.x >> 4; i < a.m * slabs; i += blockDim.x >> 4) {
+            const int r = i / slabs, col = (i - r * slabs) * kSlab + (lane & 15) * 8;
+            Eight<X> v;
+            v.load((const X*)a.a + (int64_t)r * a.ld_a + col, a.k - col);
+            const float scale = block_scale(max16(max8(v)));
+            *(uint2*)(own_codes + i * kSlab + (lane & 15) * 8) = codes8(v, 1.0f / scale);
+            if ((lane & 15) == 0) own_scales[i] = scale;
+        }
+        meet();
     }
+    while (ahead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) use(s + u * waves, some[u]);
+        s += kAhead * waves;
+        ahead = s + (kAhead - 1) * waves < full;
+        if (ahead) fetch_some();
+    }
+    for (; s < full; s += waves) {
+        fetch(s, some[0], std::true_type{});
+        use(s, some[0]);
+    }
+    if (s == full && tail) {
+        fetch(s, some[0], std::false_type{});
+        use(s, some[0]);
+    }
+
     // sums[wave][row of a][column]
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sums[wave][r16 * 16 + g * 4 + e] = acc[e];
+    for (int i = 0; i < kTiles; ++i) *(v4f*)&sums[wave][(i * 16 + r16) * 16 + g * 4] = acc[i];
     __syncthreads();
     for (int o = threadIdx.x; o < a.m * 16; o += blockDim.x) {
         float v = 0.0f;
@@ -556,17 +578,19 @@ __global__ __launch_bounds__(1024) void few_rows_kernel(ProductArgs a, int wide)
     }
 }
 
-template <class T, class X>
+template <class T, class X, int kTiles>
 void few_rows(const ProductArgs& a, hipStream_t st) {
     const int slabs = (a.k + kSlab - 1) / kSlab;
-    int waves = 1;   // as many as leave each about kAhead slabs
-    while (waves < 16 && waves * kAhead < slabs) waves *= 2;
     const unsigned grid = (unsigned)((a.n + 15) / 16);
-    const int wide = (uintptr_t)a.a % 16 == 0 && (a.ld_a * sizeof(X)) % 16 == 0;
+    // Waves so that each takes about four slabs at once; with fewer workgroups than compute units, so that each takes
+    // one: then it is latency that counts.
+    const int per = grid < 256 ? 1 : 4;
+    int waves = 1;
+    while (waves < 16 && waves * per < slabs) waves *= 2;
     if (a.b_rows == 1)
-        few_rows_kernel<T, X, true><<<grid, waves * 64, 0, st>>>(a, wide);
+        few_rows_kernel<T, X, kTiles, true><<<grid, waves * 64, 0, st>>>(a);
     else
-        few_rows_kernel<T, X, false><<<grid, waves * 64, 0, st>>>(a, wide);
+        few_rows_kernel<T, X, kTiles, false><<<grid, waves * 64, 0, st>>>(a);
 }
 
 template <class T, int BM, int BN, int WAVES_M, int WAVES_N, int kStages, int kGroups, bool kRows = true>
@@ -586,8 +610,10 @@ void product_tiles(const ProductArgs& a, hipStream_t st) {
 template <class T>
 hipError_t product(const ProductArgs& a, hipStream_t st) {
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
-    if (a.m <= kFewRows) {
-        few_rows<T, uint8_t>(a, st);
+    if (a.m <= 16) {
+        few_rows<T, uint8_t, 1>(a, st);
+    } else if (a.m <= kFewCodedRows) {
+        few_rows<T, uint8_t, 2>(a, st);
     } else if (sizeof(T) == 2 && a.b_rows == 128 && tiles(256, 256) >= 256) {
         if constexpr (sizeof(T) == 2) product_tiles<T, 256, 256, 2, 4, 2, 1, false>(a, st);
     } else if (tiles(256, 128) >= 256) {
@@ -612,13 +638,13 @@ hipError_t launch_fp8_quantize(const QuantizeArgs& a, hipStream_t st) {
     }
 }
 
-bool fp8_few_rows(int64_t m) { return m <= kFewRows; }
+bool fp8_few_rows(int64_t m, int64_t k) { return m <= kFewRows && m * ((k + 127) / 128 * 128) <= kFewNumbers; }
 
 hipError_t launch_fp8_linear_few_rows(const ProductArgs& a, hipStream_t st) {
     switch (a.out_type) {
-        case BCJR_TYPE_F32: few_rows<float, float>(a, st); break;
-        case BCJR_TYPE_BF16: few_rows<__hip_bfloat16, __hip_bfloat16>(a, st); break;
-        default: few_rows<_Float16, _Float16>(a, st); break;
+        case BCJR_TYPE_F32: few_rows<float, float, 1>(a, st); break;
+        case BCJR_TYPE_BF16: few_rows<__hip_bfloat16, __hip_bfloat16, 1>(a, st); break;
+        default: few_rows<_Float16, _Float16, 1>(a, st); break;
     }
     return hipGetLastError();
 }

@@ -192,7 +192,7 @@ int fp8_linear_backward(const void* dy, int32_t type, int64_t m, int64_t ld_dy, 
 }
 
 size_t fp8_linear_quantized_workspace_bytes(int64_t m, int64_t k) {
-    if (!dim(m) || !dim(k) || m == 0 || k == 0 || fp8_few_rows(m)) return 0;
+    if (!dim(m) || !dim(k) || m == 0 || k == 0 || fp8_few_rows(m, k)) return 0;
     return coded(m, k, 1).total;
 }
 
@@ -208,7 +208,7 @@ int fp8_linear_quantized(const void* x, int32_t type, int64_t m, int64_t ld_x, c
     const hipStream_t st = (hipStream_t)stream;
     ProductArgs p{(const uint8_t*)x, nullptr, (const uint8_t*)w, w_scale, ld_x, ld_w, (int32_t)m, (int32_t)n,
                   (int32_t)k, w_block_rows, out, ld_out, type};
-    if (fp8_few_rows(m)) return hip_status(launch_fp8_linear_few_rows(p, st));
+    if (fp8_few_rows(m, k)) return hip_status(launch_fp8_linear_few_rows(p, st));
     if (need > 0) {
         const Coded c = coded(m, k, 1).at(workspace);
         const hipError_t e = launch_fp8_quantize(quantize_args(x, type, m, k, ld_x, 1, c, Coded{}), st);

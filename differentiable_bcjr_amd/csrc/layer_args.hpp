@@ -47,7 +47,7 @@ struct OrthoArgs {
 };
 
 hipError_t launch_fp8_quantize(const QuantizeArgs& a, hipStream_t st);
-bool fp8_few_rows(int64_t m);   // whether a product of m rows quantizes them on the way
+bool fp8_few_rows(int64_t m, int64_t k);   // whether a product of m rows quantizes them on the way
 hipError_t launch_fp8_linear_few_rows(const ProductArgs& a, hipStream_t st);   // a: numbers of out_type, ld_a elements
 hipError_t launch_fp8_product(const ProductArgs& a, hipStream_t st);
 size_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols, int32_t out_type);

@@ -62,29 +62,26 @@ constexpr int kSumAhead = 4;   // loads of eight elements that a thread has in f
 
 template <class T>
 __global__ __launch_bounds__(256) void square_sum_kernel(const T* g, int rows, int cols, int64_t ld,
-                                                         int64_t batch_stride, int wide, double* partials) {
+                                                         int64_t batch_stride, double* partials) {
     __shared__ double lds[4];
     const T* p = g + (int64_t)blockIdx.y * batch_stride;
     const uint32_t across = (uint32_t)(cols + 7) / 8, count = across * (uint32_t)rows, step = gridDim.x * 256;
     double sum = 0.0;
     for (uint32_t at = blockIdx.x * 256 + threadIdx.x; at < count; at += step * kSumAhead) {
-        float v[kSumAhead][8];
+        Eight<T> v[kSumAhead];
 #pragma unroll
         for (int u = 0; u < kSumAhead; ++u) {
             const uint32_t i = at + u * step;
             const int col = i < count ? (int)(i % across) * 8 : cols;
-            const int left = cols - col;
-            if (left > 0) {
-                load8(p + (int64_t)(i / across) * ld + col, left, wide && left >= 8, v[u]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
-            }
+            v[u].load(p + (int64_t)(i / across) * ld + col, cols - col);
         }
 #pragma unroll
         for (int u = 0; u < kSumAhead; ++u)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fma((double)v[u][j], (double)v[u][j], sum);
+            for (int j = 0; j < 8; ++j) {
+                const double x = (double)v[u].at(j);
+                sum = fma(x, x, sum);
+            }
     }
     sum = block_sum(sum, lds);
     if (threadIdx.x == 0) partials[(int64_t)blockIdx.y * kPartials + blockIdx.x] = sum;
@@ -99,8 +96,8 @@ __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
 // the products' operands.  lo: X's lo halves where they lie apart, on the side that X is (kSplit: unused).
 template <class T, bool kSplit>
 __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows, int64_t cols, int64_t ld,
-                                                        int64_t batch_stride, int wide, const double* partials,
-                                                        int parts, float eps, _Float16* direct, _Float16* turned,
+                                                        int64_t batch_stride, const double* partials, int parts,
+                                                        float eps, _Float16* direct, _Float16* turned,
                                                         _Float16* lo_out, int tall, int64_t rows_p, int64_t cols_p) {
     __shared__ double lds[4];
     __shared__ uint32_t tile[64][65];   // hi | lo << 16
@@ -132,23 +129,14 @@ __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows
     const int line = t >> 2, q = (t & 3) * 16;
     uint32_t w[16];
     const int64_t left = r0 + line < rows ? cols - (c0 + q) : 0;
+    Eight<T> v[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float v[8];
-        const int here = (int)min(max(left - h * 8, (int64_t)0), (int64_t)8);
-        if (here > 0) {
-            load8(p + (r0 + line) * ld + c0 + q + h * 8, here, wide && here == 8, v);
-        } else {
+    for (int h = 0; h < 2; ++h) v[h].load(p + (r0 + line) * ld + c0 + q + h * 8, left - h * 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            _Float16 hi, lo;
-            split(j < here ? v[j] / norm * kXScale : 0.0f, hi, lo);
-            w[h * 8 + j] =
-                (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
-        }
+    for (int j = 0; j < 16; ++j) {   // what lies outside G stays 0, also where the norm is 0 or NaN
+        _Float16 hi, lo;
+        split(j < left ? v[j / 8].at(j % 8) / norm * kXScale : 0.0f, hi, lo);
+        w[j] = (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
     }
     put(direct, r0 + line, cols_p, c0 + q, w, !tall);
 #pragma unroll
@@ -595,22 +583,20 @@ template <class In>
 hipError_t orthogonalize_from(const OrthoArgs& o, hipStream_t st) {
     const Layout l = make_layout(o.batch, o.rows, o.cols, o.out_type);
     double* partials = (double*)(o.ws + l.partials);
-    const int wide = (uintptr_t)o.g % 16 == 0 && o.ld_g * (int64_t)sizeof(In) % 16 == 0 &&
-                     (o.batch == 1 || o.batch_g * (int64_t)sizeof(In) % 16 == 0);
     const int64_t chunks = o.rows * ((o.cols + 7) / 8);
     const int parts = (int)std::min<int64_t>(kPartials, (chunks + 255) / 256);
     square_sum_kernel<In><<<dim3((unsigned)parts, (unsigned)o.batch), 256, 0, st>>>(
-        (const In*)o.g, (int)o.rows, (int)o.cols, o.ld_g, o.batch_g, wide, partials);
+        (const In*)o.g, (int)o.rows, (int)o.cols, o.ld_g, o.batch_g, partials);
     auto at = [&](size_t off) { return (_Float16*)(o.ws + off); };
     const int64_t rp = pad_up(o.rows), cp = pad_up(o.cols);
     const dim3 grid((unsigned)(cp / 64), (unsigned)(rp / 64), (unsigned)o.batch);
     _Float16 *direct = at(l.tall ? l.xt[0] : l.x), *turned = at(l.tall ? l.x : l.xt[0]);
     if (l.split)
-        normalize_kernel<In, true><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, wide,
-                                                         partials, parts, o.eps, direct, turned, nullptr, l.tall, rp, cp);
+        normalize_kernel<In, true><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, partials,
+                                                         parts, o.eps, direct, turned, nullptr, l.tall, rp, cp);
     else
-        normalize_kernel<In, false><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, wide,
-                                                          partials, parts, o.eps, direct, turned, at(l.x_lo), l.tall, rp, cp);
+        normalize_kernel<In, false><<<grid, 256, 0, st>>>((const In*)o.g, o.rows, o.cols, o.ld_g, o.batch_g, partials,
+                                                          parts, o.eps, direct, turned, at(l.x_lo), l.tall, rp, cp);
     switch (o.out_type) {
         case BCJR_TYPE_F32: return iterate<true, float>(o, l, st);
         case BCJR_TYPE_BF16: return iterate<false, __hip_bfloat16>(o, l, st);

@@ -340,9 +340,9 @@ size_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
 /*
  * The layer of a served model: out [m, n] = x w^T in x's type, for weights w [n, k] quantized before (w_scale and
  * w_block_rows as b's above) and x [m, k] of `type`, quantized on the way as fp8_block_quantize does with
- * block_rows = 1.  The result is fp8_block_matmul's of those codes up to the order of its float32 sums.  Up to 16 rows
- * take one launch and no workspace; more take two and fp8_linear_quantized_workspace_bytes(m, k) bytes, 256-byte
- * aligned (BCJR_ERR_WORKSPACE).
+ * block_rows = 1.  The result is fp8_block_matmul's of those codes up to the order of its float32 sums.  Up to 4 rows
+ * of up to 32768 numbers in all take one launch and no workspace; more take two and
+ * fp8_linear_quantized_workspace_bytes(m, k) bytes, 256-byte aligned (BCJR_ERR_WORKSPACE).
  */
 int fp8_linear_quantized(const void* x, int32_t type, int64_t m, int64_t ld_x, const void* w, int64_t ld_w,
                          const float* w_scale, int32_t w_block_rows, int64_t n, int64_t k, void* out, int64_t ld_out,

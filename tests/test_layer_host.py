@@ -105,7 +105,9 @@ def test_linear_buffers():
     forward_ws = up(m * 48) + up(m * 4) + up(n * 48) + up(4)
     backward_ws = up(m * 64) + up(m * 4) + up(n * 112) + up(n * 4)
     assert ws(m, n, k) == max(forward_ws, backward_ws)
-    assert abi.fp8_linear_quantized_workspace_bytes(16, k) == 0
+    assert abi.fp8_linear_quantized_workspace_bytes(4, 8192) == abi.fp8_linear_quantized_workspace_bytes(1, 32768) == 0
+    assert abi.fp8_linear_quantized_workspace_bytes(4, 8193) == up(4 * 8208) + up(4 * 65 * 4)
+    assert abi.fp8_linear_quantized_workspace_bytes(5, k) == up(5 * 48) + up(5 * 4)
     assert abi.fp8_linear_quantized_workspace_bytes(m, k) == up(m * 48) + up(m * 4)
     assert saved(-1, n, k, 3) == ws(m, BIG, k) == abi.fp8_linear_quantized_workspace_bytes(-1, k) == 0
 
