@@ -395,7 +395,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         (full + kGroups - 1) / kGroups, mine,
         [&](int s, int slot) {
             uint8_t* stage = lds + slot * kStageBytes;
-            const int slab = s * kGroups + group;
+            const int slab = min(s * kGroups + group, full - 1);
             src_a.fetch((uint32_t)slab * kSlab, stage, wave);
             src_b.fetch((uint32_t)slab * kSlab, stage + BM * kSlab, wave);
             fetch_scales(slab, stage);

@@ -56,13 +56,14 @@ __device__ __forceinline__ void meet() {
 // The k loop: stage s of `total` is loaded into LDS slot s mod kStages, kStages - 1 stages ahead of its use.  `issue`
 // issues kLoads loads in every wave and no others are in flight; `use` reads the slot.  One meeting a stage: behind it
 // the stage is there for all waves (each has waited for its own loads), and the slot that is loaded next is no longer
-// read (it was used in the step before).  Waves that have fewer stages of their own (`mine`, at least one) load their
-// last one again, so that every wave's loads can be counted alike, and use each once.
+// read (it was used in the step before).  Waves that have fewer stages of their own (`mine`) load along, so that every
+// wave's loads can be counted alike, and do not use what they load: `issue` takes any stage below `total` and keeps
+// within the operands by itself.
 template <int kStages, int kLoads, class Issue, class Use>
 __device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s)
-        if (s < total) issue(min(s, mine - 1), s);
+        if (s < total) issue(s, s);
     int slot = 0;
 #pragma unroll 1
     for (int s = 0; s < total; ++s) {
@@ -71,7 +72,7 @@ __device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use 
         else
             wait_loads<0>();
         meet();
-        if (s + kStages - 1 < total) issue(min(s + kStages - 1, mine - 1), slot == 0 ? kStages - 1 : slot - 1);
+        if (s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
         if (s < mine) use(slot);
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }

@@ -216,12 +216,15 @@ __device__ __forceinline__ void finish(const ProdArgs& a, v4f (&acc)[TM][TN], in
     constexpr int R = TM * 16, C = TN * 16;
     static_assert(kPad % R == 0 && kPad % C == 0, "a block lies wholly inside the padded result or outside");
     if (row0 >= a.rows || col0 >= a.cols) return;
+    if constexpr (kMode == kGram) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        if constexpr (kMode == kGram) {
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] *= a.alpha;
-        } else {
+    } else {
+        v4h hi[TM][TN], lo[TM][TN];   // all loads, then their uses
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
             const int64_t row = row0 + i * 16 + r16;
             const _Float16* old = a.old + o + row * ld + (int64_t)col0 * H::kPer + g * 4;
             const _Float16* old_lo = old + 32;
@@ -229,17 +232,22 @@ __device__ __forceinline__ void finish(const ProdArgs& a, v4f (&acc)[TM][TN], in
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int at = (int)H::at(j * 16);
-                const v4h hi = *(const v4h*)(old + at);
-                v4h lo = {0, 0, 0, 0};
-                if constexpr (kSplit || kMode == kStep) lo = *(const v4h*)(old_lo + at);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = fmaf(a.alpha, (float)hi[e] + (float)lo[e], a.beta * acc[i][j][e]);
+                hi[i][j] = *(const v4h*)(old + at);
+                if constexpr (kSplit || kMode == kStep) lo[i][j] = *(const v4h*)(old_lo + at);
             }
-            __builtin_amdgcn_sched_barrier(0);   // a row's loads at a time: all at once take too many registers
         }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = (float)hi[i][j][e];
+                    if constexpr (kSplit || kMode == kStep) x += (float)lo[i][j][e];
+                    acc[i][j][e] = fmaf(a.alpha, x, a.beta * acc[i][j][e]);
+                }
     }
-
     forget();
     if (kMode == kStep && a.out) {
         T* out = (T*)a.out + item * a.out_batch;
@@ -382,7 +390,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void ortho_pro
         (last - first + kGroups - 1) / kGroups, (last - first - group + kGroups - 1) / kGroups,
         [&](int s, int slot) {
             uint8_t* stage = lds + slot * kStageBytes;
-            const uint32_t at = (uint32_t)(first + s * kGroups + group) * kSlab;
+            const uint32_t at = (uint32_t)min(first + s * kGroups + group, last - 1) * kSlab;
             src_p.fetch(at, stage, wave);
             src_q.fetch(at, stage + BM * kSlab, wave);
         },
@@ -500,12 +508,12 @@ inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, boo
     constexpr int64_t kCus = 256;
     const int64_t slabs = k / slab_cols;
     if (tiles(256) >= kCus * 3 / 4) return {256, 1, 1};
-    if (symmetric && tiles(256) >= 24) {
-        const int64_t parts = std::min(kCus / tiles(256), slabs / 8);
+    if (symmetric && tiles(256) >= 24 && slabs >= 64) {
+        const int64_t parts = kCus / tiles(256);
         if (parts > 1) return {256, (int)parts, 1};
     }
     if (tiles(128) > kCus) return {128, 1, 1};
-    if (tiles(128) >= kCus * 3 / 4) return {128, 1, 2};
+    if (tiles(128) >= kCus / 2 && slabs >= 4) return {128, 1, 2};
     return {64, 1, tiles(64) <= kCus && slabs >= 4 ? 2 : 1};
 }
 

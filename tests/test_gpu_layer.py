@@ -442,6 +442,18 @@ def test_orthogonalize_stacks_and_strides(dev, dtype):
     assert dba.orthogonalize(g[:0]).shape == (0, 150, 90) and dba.orthogonalize(g[:, :0]).shape == (6, 0, 90)
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(130, 64, 64), (130, 20, 100), (40, 64, 520), (260, 16, 40), (20, 200, 300)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_orthogonalize_many_small(dev, batch, rows, cols, dtype):
+    """Stacks that fill the card with matrices of one or few k steps each."""
+    g = torch.stack([_update("plain", rows, cols, s) for s in range(3)]).to(dtype)
+    got = dba.orthogonalize(g[torch.arange(batch) % 3].to(dev))
+    for i in (0, 1, 2):
+        _check_orthogonal(got[i], g[i].float(), 5, USUAL, 1e-7, dtype)
+        same = got[torch.arange(batch) % 3 == i]
+        assert torch.equal(same, got[i].expand_as(same))
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 
