@@ -257,6 +257,24 @@ __device__ __forceinline__ void block_products(const Halves (&b)[TN], const Halv
         for (int j = 0; j < TN; ++j) p[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j].h[h], a.h[h], p[j], 0, 0, 0);
 }
 
+// Every fragment of a with every one of b.
+template <int TM, int TN, int N>
+__device__ __forceinline__ void tile_products(const v8i (&b)[TN], const v8i (&a)[TM], v4f (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = block_product(b[i % TN], a[i / TN]);
+}
+
+template <int TM, int TN, int N>
+__device__ __forceinline__ void tile_products(const Halves (&b)[TN], const Halves (&a)[TM], v4f (&p)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[i % TN].h[h], a[i / TN].h[h], p[i], 0, 0, 0);
+}
+
 __device__ __forceinline__ void take(v8i codes, v8i& out) { out = codes; }
 __device__ __forceinline__ void take(v8i codes, Halves& out) { out = widen(codes); }
 
@@ -309,10 +327,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         scale_step = kRowScales ? (uint32_t)a.n : (uint32_t)((a.n + 127) / 128);
         scale_lane = (uint32_t)(kRowScales ? n : n / 128);
     }
-    auto fetch_scales = [&](int s, uint8_t* stage) {
+    auto scale_at = [&] {
         uint32_t at = scale_lane * 4;
         asm("" : "+v"(at));
-        load4_to_lds((const uint8_t*)(scales + (int64_t)s * scale_step) + at, stage + kScalesAt + part * 256);
+        return at;
     };
 
     v4f acc[TM][TN];
@@ -335,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         for (int j = 0; j < TN; ++j) take(read_slab(lb, wn0 + j * 16 + r16, g), fb[j]);
         take(read_slab(la, wm0 + r16, g), fa[0]);
         v8i raw;   // codes that are yet to be widened
-        if constexpr (kWide && TM > 1) raw = read_slab(la, wm0 + 16 + r16, g);
+        if constexpr (kWide && TM * TN > 4) raw = read_slab(la, wm0 + 16 + r16, g);
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = ls[wm0 + i * 16 + r16];
         if constexpr (kRowScales) {
@@ -345,6 +363,22 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
             const float b = ls[BM + wn0];
 #pragma unroll
             for (int i = 0; i < TM; ++i) sa[i] *= b;
+        }
+        if constexpr (TM * TN <= 4) {   // all at once: it takes every tile's MFMAs to cover one's latency
+#pragma unroll
+            for (int i = 1; i < TM; ++i) take(read_slab(la, wm0 + i * 16 + r16, g), fa[i]);
+            v4f p[TM * TN];
+            tile_products(fb, fa, p);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = kRowScales ? p[i * TN + j][e] * sb[kRowScales ? j : 0][e] : p[i * TN + j][e];
+                        acc[i][j][e] = fmaf(v, sa[i], acc[i][j][e]);
+                    }
+            return;
         }
         v4f p[2][TN];
         __builtin_amdgcn_sched_barrier(0);
@@ -388,30 +422,37 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         }
     };
 
-    // group i takes the whole slabs i, i + kGroups, ..., the last group also the cut one
+    // Group i takes the whole slabs i, i + kGroups, ...; the last group takes the cut one first, from the slot that the
+    // stages ahead leave free, so that its loads wait along with theirs.
     const int full = a.k / kSlab, tail = a.k % kSlab;
-    const int mine = (full - group + kGroups - 1) / kGroups;
-    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + 1>(
-        (full + kGroups - 1) / kGroups, mine,
-        [&](int s, int slot) {
-            uint8_t* stage = lds + slot * kStageBytes;
-            const int slab = min(s * kGroups + group, full - 1);
-            src_a.fetch((uint32_t)slab * kSlab, stage, wave);
-            src_b.fetch((uint32_t)slab * kSlab, stage + BM * kSlab, wave);
-            fetch_scales(slab, stage);
-        },
-        [&](int slot) { multiply(lds + slot * kStageBytes); });
+    const auto issue = [&](int s, int slot) {
+        uint8_t* stage = lds + slot * kStageBytes;
+        const int slab = min(s * kGroups + group, full - 1);
+        src_a.fetch((uint32_t)slab * kSlab, stage, wave);
+        src_b.fetch((uint32_t)slab * kSlab, stage + BM * kSlab, wave);
+        load4_to_lds((const uint8_t*)(scales + (int64_t)slab * scale_step) + scale_at(), stage + kScalesAt + part * 256);
+    };
+    const int total = (full + kGroups - 1) / kGroups;
+    if (tail && group == kGroups - 1) {
+        TailSlab<BM, kWaves> tail_a;
+        TailSlab<BN, kWaves> tail_b;
+        tail_a.load(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, wave, lane);
+        tail_b.load(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, wave, lane);
+        const float scale = scales[(int64_t)full * scale_step + scale_lane];
+        pipeline_ahead<kStages>(total, issue);
+        uint8_t* stage = lds + (kStages - 1) * kStageBytes;
+        tail_a.put(stage, wave, lane);
+        tail_b.put(stage + BM * kSlab, wave, lane);
+        *(float*)(stage + kScalesAt + part * 256 + lane * 4) = scale;
+    } else {
+        pipeline_ahead<kStages>(total, issue);
+    }
     if (tail) {
         meet();
-        if (group == kGroups - 1) {
-            fetch_scales(full, lds);
-            fetch_tail<BM, kWaves>(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, lds, wave, lane);
-            fetch_tail<BN, kWaves>(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, lds + BM * kSlab, wave, lane);
-            wait_loads<0>();
-        }
-        meet();
-        if (group == kGroups - 1) multiply(lds);
+        if (group == kGroups - 1) multiply(lds + (kStages - 1) * kStageBytes);
     }
+    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + 1>(
+        total, (full - group + kGroups - 1) / kGroups, issue, [&](int slot) { multiply(lds + slot * kStageBytes); });
 
     using Tile = WaveTile<T, TM * 16, TN * 16>;
     constexpr int kJoinAt = kWaves * Tile::kBytes, kJoinBytes = (kGroups - 1) * kWaves * TM * TN * 1024;

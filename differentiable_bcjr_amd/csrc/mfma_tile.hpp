@@ -59,11 +59,17 @@ __device__ __forceinline__ void meet() {
 // read (it was used in the step before).  Waves that have fewer stages of their own (`mine`) load along, so that every
 // wave's loads can be counted alike, and do not use what they load: `issue` takes any stage below `total` and keeps
 // within the operands by itself.
-template <int kStages, int kLoads, class Issue, class Use>
-__device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
+//
+// The first kStages - 1 stages' loads; slot kStages - 1 is free until pipelined() begins.
+template <int kStages, class Issue>
+__device__ __forceinline__ void pipeline_ahead(int total, Issue issue) {
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s)
         if (s < total) issue(s, s);
+}
+
+template <int kStages, int kLoads, class Issue, class Use>
+__device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
     int slot = 0;
 #pragma unroll 1
     for (int s = 0; s < total; ++s) {
@@ -149,18 +155,26 @@ __device__ __forceinline__ v4i load_chunk(const uint8_t* row, int at, int length
     return v;
 }
 
-// The slab behind the last whole one of a row of `length` bytes (kbyte: where it begins).
+// The slab behind the last whole one of rows of `length` bytes (kbyte: where it begins), through registers.
 template <int ROWS, int NW>
-__device__ __forceinline__ void fetch_tail(const uint8_t* base, uint32_t ld, int rows, int kbyte, int length,
-                                           uint8_t* lds, int wave, int lane) {
-#pragma unroll 1
-    for (int i = 0; i < ROWS / (8 * NW); ++i) {
-        const int part = i * NW + wave;
-        const int row = part * 8 + (lane >> 3);
-        const uint8_t* p = base + (size_t)((uint32_t)min(row, rows - 1) * ld);
-        *(v4i*)(lds + part * 1024 + lane * 16) = load_chunk(p, kbyte + (int)slab_chunk(row, lane & 7) * 16, length);
+struct TailSlab {
+    static constexpr int kLoads = ROWS / (8 * NW);
+    v4i v[kLoads];
+
+    __device__ __forceinline__ void load(const uint8_t* base, uint32_t ld, int rows, int kbyte, int length, int wave,
+                                         int lane) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = (i * NW + wave) * 8 + (lane >> 3);
+            v[i] = load_chunk(base + (size_t)((uint32_t)min(row, rows - 1) * ld),
+                              kbyte + (int)slab_chunk(row, lane & 7) * 16, length);
+        }
     }
-}
+    __device__ __forceinline__ void put(uint8_t* lds, int wave, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) *(v4i*)(lds + (i * NW + wave) * 1024 + lane * 16) = v[i];
+    }
+};
 
 // Chunks g and g + 4 of row `row`.
 __device__ __forceinline__ v8i read_slab(const uint8_t* lds, int row, int g) {

@@ -386,14 +386,16 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void ortho_pro
     const int wm0 = wm * TM * 16, wn0 = wn * TN * 16;
 
     // group i takes slabs first + i, first + i + kGroups, ...
+    const auto issue = [&](int s, int slot) {
+        uint8_t* stage = lds + slot * kStageBytes;
+        const uint32_t at = (uint32_t)min(first + s * kGroups + group, last - 1) * kSlab;
+        src_p.fetch(at, stage, wave);
+        src_q.fetch(at, stage + BM * kSlab, wave);
+    };
+    const int total = (last - first + kGroups - 1) / kGroups;
+    pipeline_ahead<kStages>(total, issue);
     pipelined<kStages, 2 * Source::kLoads>(
-        (last - first + kGroups - 1) / kGroups, (last - first - group + kGroups - 1) / kGroups,
-        [&](int s, int slot) {
-            uint8_t* stage = lds + slot * kStageBytes;
-            const uint32_t at = (uint32_t)min(first + s * kGroups + group, last - 1) * kSlab;
-            src_p.fetch(at, stage, wave);
-            src_q.fetch(at, stage + BM * kSlab, wave);
-        },
+        total, (last - first - group + kGroups - 1) / kGroups, issue,
         [&](int slot) {
             const uint8_t* lp = lds + slot * kStageBytes;
             const uint8_t* lq = lp + BM * kSlab;
