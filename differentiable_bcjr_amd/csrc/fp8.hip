@@ -287,8 +287,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
     constexpr bool kWide = sizeof(T) == 4;
     constexpr int TM = BM / WAVES_M / 16, TN = BN / WAVES_N / 16;
     constexpr int kScalesAt = (BM + BN) * kSlab, kStageBytes = kScalesAt + (BM + BN) * 4;
-    constexpr int kScaleLoads = (BM + BN) / 64;   // of 64 scales each; waves beyond that repeat one
-    static_assert(kScaleLoads <= kWaves, "one load of scales a wave");
+    constexpr int kScaleLoads = (BM + BN) / 64;                          // of 64 scales each, shared by the waves;
+    constexpr int kScalePer = (kScaleLoads + kWaves - 1) / kWaves;       // where they do not come out even, some twice
     static_assert(kRowScales || 128 % (BN / WAVES_N) == 0, "a wave's columns lie in one block of b");
     using Frag = std::conditional_t<kWide, Halves, v8i>;
     __shared__ __align__(1024) uint8_t all_lds[kGroups * kStages * kStageBytes];
@@ -313,25 +313,24 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
     src_a.set(pa, (uint32_t)a.ld_a, rows_a, wave, lane);
     src_b.set(pb, (uint32_t)a.ld_b, rows_b, wave, lane);
 
-    // this wave's 64 scales of a stage
-    const int part = wave % kScaleLoads;
-    const float* scales;
-    uint32_t scale_step, scale_lane;
-    if (part < BM / 64) {
-        scales = a.a_scale;
-        scale_step = (uint32_t)a.m;
-        scale_lane = (uint32_t)min(m0 + part * 64 + lane, a.m - 1);
-    } else {
-        const int n = min(n0 + (part - BM / 64) * 64 + lane, a.n - 1);
-        scales = a.b_scale;
-        scale_step = kRowScales ? (uint32_t)a.n : (uint32_t)((a.n + 127) / 128);
-        scale_lane = (uint32_t)(kRowScales ? n : n / 128);
+    // this wave's scales of a stage, 64 a load
+    const float* scales[kScalePer];
+    uint32_t scale_step[kScalePer], scale_lane[kScalePer];
+    int part[kScalePer];
+#pragma unroll
+    for (int x = 0; x < kScalePer; ++x) {
+        part[x] = (wave + x * kWaves) % kScaleLoads;
+        if (part[x] < BM / 64) {
+            scales[x] = a.a_scale;
+            scale_step[x] = (uint32_t)a.m;
+            scale_lane[x] = (uint32_t)min(m0 + part[x] * 64 + lane, a.m - 1) * 4;
+        } else {
+            const int n = min(n0 + (part[x] - BM / 64) * 64 + lane, a.n - 1);
+            scales[x] = a.b_scale;
+            scale_step[x] = kRowScales ? (uint32_t)a.n : (uint32_t)((a.n + 127) / 128);
+            scale_lane[x] = (uint32_t)(kRowScales ? n : n / 128) * 4;
+        }
     }
-    auto scale_at = [&] {
-        uint32_t at = scale_lane * 4;
-        asm("" : "+v"(at));
-        return at;
-    };
 
     v4f acc[TM][TN];
 #pragma unroll
@@ -430,7 +429,13 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         const int slab = min(s * kGroups + group, full - 1);
         src_a.fetch((uint32_t)slab * kSlab, stage, wave);
         src_b.fetch((uint32_t)slab * kSlab, stage + BM * kSlab, wave);
-        load4_to_lds((const uint8_t*)(scales + (int64_t)slab * scale_step) + scale_at(), stage + kScalesAt + part * 256);
+#pragma unroll
+        for (int x = 0; x < kScalePer; ++x) {
+            uint32_t at = scale_lane[x];
+            asm("" : "+v"(at));
+            load4_to_lds((const uint8_t*)(scales[x] + (int64_t)slab * scale_step[x]) + at,
+                         stage + kScalesAt + part[x] * 256);
+        }
     };
     const int total = (full + kGroups - 1) / kGroups;
     if (tail && group == kGroups - 1) {
@@ -438,21 +443,22 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
         TailSlab<BN, kWaves> tail_b;
         tail_a.load(pa, (uint32_t)a.ld_a, rows_a, full * kSlab, a.k, wave, lane);
         tail_b.load(pb, (uint32_t)a.ld_b, rows_b, full * kSlab, a.k, wave, lane);
-        const float scale = scales[(int64_t)full * scale_step + scale_lane];
-        pipeline_ahead<kStages>(total, issue);
+        float scale[kScalePer];
+#pragma unroll
+        for (int x = 0; x < kScalePer; ++x)
+            scale[x] = *(const float*)((const uint8_t*)(scales[x] + (int64_t)full * scale_step[x]) + scale_lane[x]);
         uint8_t* stage = lds + (kStages - 1) * kStageBytes;
+        pipeline_ahead<kStages>(total, issue);
         tail_a.put(stage, wave, lane);
         tail_b.put(stage + BM * kSlab, wave, lane);
-        *(float*)(stage + kScalesAt + part * 256 + lane * 4) = scale;
+#pragma unroll
+        for (int x = 0; x < kScalePer; ++x) *(float*)(stage + kScalesAt + part[x] * 256 + lane * 4) = scale[x];
     } else {
         pipeline_ahead<kStages>(total, issue);
     }
-    if (tail) {
-        meet();
-        if (group == kGroups - 1) multiply(lds + (kStages - 1) * kStageBytes);
-    }
-    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + 1>(
-        total, (full - group + kGroups - 1) / kGroups, issue, [&](int slot) { multiply(lds + slot * kStageBytes); });
+    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + kScalePer>(
+        tail ? -1 : 0, total, group == kGroups - 1, (full - group + kGroups - 1) / kGroups, issue,
+        [&](int slot) { multiply(lds + slot * kStageBytes); });
 
     using Tile = WaveTile<T, TM * 16, TN * 16>;
     constexpr int kJoinAt = kWaves * Tile::kBytes, kJoinBytes = (kGroups - 1) * kWaves * TM * TN * 1024;

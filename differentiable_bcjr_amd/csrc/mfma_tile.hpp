@@ -60,26 +60,27 @@ __device__ __forceinline__ void meet() {
 // wave's loads can be counted alike, and do not use what they load: `issue` takes any stage below `total` and keeps
 // within the operands by itself.
 //
-// The first kStages - 1 stages' loads; slot kStages - 1 is free until pipelined() begins.
+// The first kStages - 1 stages' loads go out in pipeline_ahead().  Slot kStages - 1 is free until pipelined() begins: with
+// `first` -1 that slot's contents, written in between, are used ahead of stage 0 by the waves with `mine_first`.  Loops
+// are kept as loops: a kernel of a few microseconds runs most of its code once, from a cold instruction cache.
 template <int kStages, class Issue>
 __device__ __forceinline__ void pipeline_ahead(int total, Issue issue) {
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s)
-        if (s < total) issue(s, s);
+#pragma unroll 1
+    for (int s = 0; s < min(kStages - 1, total); ++s) issue(s, s);
 }
 
 template <int kStages, int kLoads, class Issue, class Use>
-__device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
-    int slot = 0;
+__device__ __forceinline__ void pipelined(int first, int total, bool mine_first, int mine, Issue issue, Use use) {
+    int slot = first < 0 ? kStages - 1 : 0;
 #pragma unroll 1
-    for (int s = 0; s < total; ++s) {
+    for (int s = first; s < total; ++s) {
         if (s + kStages - 1 <= total)
             wait_loads<kLoads*(kStages - 2)>();
         else
             wait_loads<0>();
         meet();
-        if (s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-        if (s < mine) use(slot);
+        if (s >= 0 && s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+        if (s < 0 ? mine_first : s < mine) use(slot);
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }
 }
@@ -140,17 +141,20 @@ struct SlabSource {
 };
 
 // Bytes at .. at + 15 of a row of `length` bytes that starts at `row`, zeros behind its end.  The row starts on a
-// 16-byte boundary.  In the chunk that the end cuts, each byte is loaded by itself (sixteen independent loads).
+// 16-byte boundary; nothing behind its end is read: where the end cuts the chunk, the row's last 16 bytes are, and moved
+// into place.
 __device__ __forceinline__ v4i load_chunk(const uint8_t* row, int at, int length) {
+    typedef v4i v4i_byte __attribute__((aligned(1)));
     v4i v = {0, 0, 0, 0};
     if (at + 16 <= length) {
         v = *(const v4i*)(row + at);
     } else if (at < length) {
-        uint32_t byte[16];
-#pragma unroll
-        for (int b = 0; b < 16; ++b) byte[b] = row[min(at + b, length - 1)];
-#pragma unroll
-        for (int b = 0; b < 16; ++b) v[b >> 2] |= (int)(at + b < length ? byte[b] << ((b & 3) * 8) : 0u);
+        if (length >= 16) {
+            unsigned __int128 w = __builtin_bit_cast(unsigned __int128, (v4i)*(const v4i_byte*)(row + length - 16));
+            v = __builtin_bit_cast(v4i, w >> ((at + 16 - length) * 8));
+        } else {
+            for (int b = 0; b < length; ++b) v[b >> 2] |= (int)row[b] << ((b & 3) * 8);   // at is 0
+        }
     }
     return v;
 }
