@@ -456,8 +456,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
     } else {
         pipeline_ahead<kStages>(total, issue);
     }
-    pipelined<kStages, SourceA::kLoads + SourceB::kLoads + kScalePer>(
-        tail ? -1 : 0, total, group == kGroups - 1, (full - group + kGroups - 1) / kGroups, issue,
+    pipelined_after<kStages, SourceA::kLoads + SourceB::kLoads + kScalePer>(
+        tail != 0, group == kGroups - 1, total, (full - group + kGroups - 1) / kGroups, issue,
         [&](int slot) { multiply(lds + slot * kStageBytes); });
 
     using Tile = WaveTile<T, TM * 16, TN * 16>;

@@ -60,27 +60,45 @@ __device__ __forceinline__ void meet() {
 // wave's loads can be counted alike, and do not use what they load: `issue` takes any stage below `total` and keeps
 // within the operands by itself.
 //
-// The first kStages - 1 stages' loads go out in pipeline_ahead().  Slot kStages - 1 is free until pipelined() begins: with
-// `first` -1 that slot's contents, written in between, are used ahead of stage 0 by the waves with `mine_first`.  Loops
-// are kept as loops: a kernel of a few microseconds runs most of its code once, from a cold instruction cache.
+// The first kStages - 1 stages' loads go out in pipeline_ahead(); slot kStages - 1 is free until pipelined() begins.
 template <int kStages, class Issue>
 __device__ __forceinline__ void pipeline_ahead(int total, Issue issue) {
-#pragma unroll 1
-    for (int s = 0; s < min(kStages - 1, total); ++s) issue(s, s);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s)
+        if (s < total) issue(s, s);
 }
 
 template <int kStages, int kLoads, class Issue, class Use>
-__device__ __forceinline__ void pipelined(int first, int total, bool mine_first, int mine, Issue issue, Use use) {
-    int slot = first < 0 ? kStages - 1 : 0;
+__device__ __forceinline__ void pipelined(int total, int mine, Issue issue, Use use) {
+    int slot = 0;
 #pragma unroll 1
-    for (int s = first; s < total; ++s) {
+    for (int s = 0; s < total; ++s) {
+        if (s + kStages - 1 <= total)
+            wait_loads<kLoads*(kStages - 2)>();
+        else
+            wait_loads<0>();
+        meet();
+        if (s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+        if (s < mine) use(slot);
+        slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+}
+
+// pipelined() with a stage before the first where `lead` says so: slot kStages - 1 as it was written in between, used by
+// the waves with `mine_lead`.  (The loop starts one stage early; a second copy of `use` would cost the small products,
+// which run most of their code once from a cold instruction cache.)
+template <int kStages, int kLoads, class Issue, class Use>
+__device__ __forceinline__ void pipelined_after(bool lead, bool mine_lead, int total, int mine, Issue issue, Use use) {
+    int slot = lead ? kStages - 1 : 0;
+#pragma unroll 1
+    for (int s = lead ? -1 : 0; s < total; ++s) {
         if (s + kStages - 1 <= total)
             wait_loads<kLoads*(kStages - 2)>();
         else
             wait_loads<0>();
         meet();
         if (s >= 0 && s + kStages - 1 < total) issue(s + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
-        if (s < 0 ? mine_first : s < mine) use(slot);
+        if (s < 0 ? mine_lead : s < mine) use(slot);
         slot = slot + 1 == kStages ? 0 : slot + 1;
     }
 }

@@ -395,7 +395,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void ortho_pro
     const int total = (last - first + kGroups - 1) / kGroups;
     pipeline_ahead<kStages>(total, issue);
     pipelined<kStages, 2 * Source::kLoads>(
-        0, total, false, (last - first - group + kGroups - 1) / kGroups, issue,
+        total, (last - first - group + kGroups - 1) / kGroups, issue,
         [&](int slot) {
             const uint8_t* lp = lds + slot * kStageBytes;
             const uint8_t* lq = lp + BM * kSlab;
