@@ -496,8 +496,11 @@ void launch_tiles(ProdArgs a, int64_t batch, int parts, hipStream_t st) {
     }
 }
 
-// How a product over k is cut: tiles of 256 (a symmetric product's in `parts` parts of the k loop where they leave most
-// of the card idle), of 128 or of 64, the k loop of a tile shared by `groups` groups of waves.
+// How a product over k is cut: tiles of 256, of 128 or of 64, as large as leave most of the card busy; the k loop of a
+// tile shared by `groups` groups of waves, which meet in LDS; and a symmetric product's k loop in `parts` parts, which
+// meet in a second kernel.  Parts pay where few tiles stand against a long k: 2048 x 2048 over k = 8192 for a float32
+// result takes 104 + 17 us in 7 parts of 36 tiles of 256 and 167 us in 136 tiles of 128, over k = 2048 37 + 19 us and
+// 54 us, and with the hi halves alone 22 + 11 us and 26 us.
 struct Cut {
     int tile, parts, groups;
 };
@@ -510,12 +513,11 @@ inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, boo
     constexpr int64_t kCus = 256;
     const int64_t slabs = k / slab_cols;
     if (tiles(256) >= kCus * 3 / 4) return {256, 1, 1};
-    if (symmetric && tiles(256) >= 24 && slabs >= 64) {
-        const int64_t parts = kCus / tiles(256);
-        if (parts > 1) return {256, (int)parts, 1};
-    }
+    if (symmetric && tiles(256) >= 24 && slabs >= 64) return {256, (int)std::max<int64_t>(1, kCus / tiles(256)), 1};
     if (tiles(128) > kCus) return {128, 1, 1};
     if (tiles(128) >= kCus / 2 && slabs >= 4) return {128, 1, 2};
+    if (symmetric && tiles(64) <= kCus / 4 && slabs >= 64)
+        return {64, (int)std::min(kCus / tiles(64), slabs / 16), 1};
     return {64, 1, tiles(64) <= kCus && slabs >= 4 ? 2 : 1};
 }
 
@@ -531,7 +533,7 @@ void launch_product(const ProdArgs& a, int64_t batch, hipStream_t st) {
     else if (c.groups == 2)
         launch_tiles<kMode, kSplit, T, 64, 2, 2, 4, 2>(a, batch, 1, st);
     else
-        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4, 1>(a, batch, 1, st);
+        launch_tiles<kMode, kSplit, T, 64, 2, 2, 4, 1>(a, batch, c.parts, st);
 }
 
 template <bool kSplit, class Out>

@@ -384,7 +384,7 @@ def _check_orthogonal(got, g, steps, coefficients, eps, out_dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 300), (300, 1), (7, 5), (16, 16), (64, 64), (65, 130), (128, 128),
-                                       (200, 100), (129, 1000), (520, 300)])
+                                       (200, 100), (129, 1000), (520, 300), (50, 4200), (8300, 60), (130, 4100)])
 def test_orthogonalize_sizes(dev, rows, cols, dtype):
     g = _update("plain", rows, cols, rows + cols).to(dtype)
     _check_orthogonal(dba.orthogonalize(g.to(dev)), g.float(), 5, USUAL, 1e-7, dtype)
