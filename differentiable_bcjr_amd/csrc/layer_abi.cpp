@@ -14,7 +14,10 @@ using namespace bcjr;
 
 constexpr int64_t kMaxDim = (int64_t)1 << 23;       // rows, columns and reduction lengths of the 8-bit operators
 constexpr int64_t kMaxDistance = (int64_t)1 << 23;  // bytes between the rows of 8-bit operands: a tile's 256 rows within 2^31
-constexpr int64_t kMaxTiles = ((int64_t)1 << 31) - 1;
+// Grids stay under 2^32 threads: a product's results in tiles of 16 x 16 (the kernels' tiles are 128 to 256 times as
+// large, with 512 threads), a quantization's blocks of 256 threads for 16 x 128 numbers.
+constexpr int64_t kMaxTiles = (int64_t)1 << 29;
+constexpr int64_t kMaxQuantizeBlocks = (int64_t)1 << 23;
 constexpr int64_t kMaxUpdateDim = 65536;
 constexpr int64_t kMaxBatch = 65535;                // a grid's third dimension
 constexpr int32_t kMaxSteps = 1000;
@@ -74,8 +77,11 @@ SavedPlan saved_plan(int64_t m, int64_t n, int64_t k, int32_t grads) {
 // Sizes for which every product of the layer and its gradients is within one grid.
 bool linear_dims(int64_t m, int64_t n, int64_t k) {
     if (!dim(m) || !dim(n) || !dim(k)) return false;
-    const int64_t a = blocks(m, 16), b = blocks(n, 16), c = blocks(k, 16);
-    return a * b <= kMaxTiles && a * c <= kMaxTiles && b * c <= kMaxTiles;
+    const auto fits = [](int64_t rows, int64_t cols) {
+        return blocks(rows, 16) * blocks(cols, 16) <= kMaxTiles &&
+               blocks(rows, 16) * blocks(cols, 128) <= kMaxQuantizeBlocks;
+    };
+    return fits(m, n) && fits(m, k) && fits(n, k);
 }
 
 bool scratch(const void* p, size_t bytes, size_t need) {
@@ -108,7 +114,7 @@ int fp8_block_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, 
     if (rows == 0 || cols == 0) return BCJR_OK;
     if (!x || !q || !scale || (q_t == nullptr) != (scale_t == nullptr)) return BCJR_ERR_NULL;
     if (ld_x < cols || !rows16(q, ld_q, cols) || (q_t && !rows16(q_t, ld_qt, rows))) return BCJR_ERR_LAYOUT;
-    if (blocks(rows, 16) * blocks(cols, 128) > kMaxTiles) return BCJR_ERR_SIZE;
+    if (blocks(rows, 16) * blocks(cols, 128) > kMaxQuantizeBlocks) return BCJR_ERR_SIZE;
     const QuantizeArgs a{x, type, block_rows, rows, cols, ld_x, (uint8_t*)q, ld_q, scale, (uint8_t*)q_t, ld_qt, scale_t};
     return hip_status(launch_fp8_quantize(a, (hipStream_t)stream));
 }

@@ -280,7 +280,8 @@ int bcjr_soft_codeword_noalloc(const float* w, const float* codebook, int64_t B,
  * layer, and turn the gradient of the weights into an update.  As above, every tensor pointer is a device pointer owned
  * by the caller, nothing is allocated or synchronized, and every check but BCJR_ERR_HIP runs before any launch.  Row
  * distances (ld_*) are in elements of the array.  Matrices with no rows or no columns are accepted and leave their
- * outputs untouched (a product over k = 0 writes zeros).  Row counts, column counts and k are at most 2^23.
+ * outputs untouched (a product over k = 0 writes zeros).  Row counts, column counts and k of the 8-bit
+ * operators are at most 2^23, a quantized matrix has at most 2^34 entries and a product 2^37 (BCJR_ERR_SIZE).
  */
 enum { BCJR_TYPE_F32 = 0, BCJR_TYPE_BF16 = 1, BCJR_TYPE_F16 = 2 };
 

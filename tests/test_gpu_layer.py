@@ -260,6 +260,55 @@ def test_linear_keeps_leading_dimensions_and_skips_what_is_not_asked(dev):
     assert torch.equal(dba.fp8_linear_quantized(x, q, s), want)
 
 
+def test_linear_takes_one_token_an_empty_sum_and_a_broadcast_gradient(dev):
+    x, w, _ = _linear_case(6, 40, 50, torch.float32)
+    x, w = x.to(dev), w.to(dev)
+    q, s = dba.fp8_block_quantize(w, block_rows=128)
+    one = dba.fp8_linear(x[0], w)
+    assert one.shape == (40,) and torch.equal(one, dba.fp8_linear(x[:1], w)[0])
+    one = dba.fp8_linear_quantized(x[0], q, s)
+    assert one.shape == (40,) and torch.equal(one, dba.fp8_linear_quantized(x[:1], q, s)[0])
+    for rows in (1, 30):   # k = 0
+        nothing = dba.fp8_block_quantize(w[:, :0], block_rows=128)
+        assert torch.equal(dba.fp8_linear_quantized(x.new_empty(rows, 0), *nothing), torch.zeros(rows, 40, device=dev))
+    xg, wg = x.view(2, 3, 50).clone().requires_grad_(True), w.clone().requires_grad_(True)
+    dba.fp8_linear(xg, wg).sum().backward()   # an upstream gradient of one number with strides of 0
+    want = torch.autograd.grad(dba.fp8_linear(xg, wg), (xg, wg), torch.ones(2, 3, 40, device=dev))
+    assert torch.equal(xg.grad, want[0]) and torch.equal(wg.grad, want[1])
+    y = dba.fp8_linear(xg, wg)
+    (first,) = torch.autograd.grad(y.square().sum(), xg, create_graph=True)
+    with pytest.raises(RuntimeError):   # the gradient has none of its own
+        first.sum().backward()
+
+
+def test_linear_step_in_a_graph(dev):
+    """Forward and both gradients captured together and replayed on new inputs, against the eager step."""
+    x, w, dy = (t.to(dev) for t in _linear_case(70, 140, 150, torch.bfloat16))
+    xs, ws = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(dba.fp8_linear(xs, ws), (xs, ws), dy)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = dba.fp8_linear(xs, ws)
+        dx, dw = torch.autograd.grad(y, (xs, ws), dy)
+    y = y.detach()
+    for seed in (31, 32, 33):
+        nx, nw, ndy = (t.to(dev) for t in _linear_case(70, 140, 150, torch.bfloat16, seed=seed))
+        with torch.no_grad():
+            xs.copy_(nx)
+            ws.copy_(nw)
+            dy.copy_(ndy)
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = nx.requires_grad_(True), nw.requires_grad_(True)
+        want = dba.fp8_linear(a, b)
+        grads = torch.autograd.grad(want, (a, b), ndy)
+        assert torch.equal(y, want) and torch.equal(dx, grads[0]) and torch.equal(dw, grads[1])
+
+
 def test_linear_without_tokens(dev):
     w = torch.randn(8, 32, device=dev, requires_grad=True)
     x = torch.empty(0, 32, device=dev, requires_grad=True)

@@ -49,6 +49,8 @@ def ortho(g=P, type=0, batch=1, rows=8, cols=8, ld=8, batch_g=64, steps=5, a=1.0
     (dict(ld_q=24), abi.BCJR_ERR_LAYOUT), (dict(cols=17, ld=17), abi.BCJR_ERR_LAYOUT),
     (dict(q_t=P + 1, s_t=P), abi.BCJR_ERR_LAYOUT), (dict(q_t=P, s_t=P, rows=17), abi.BCJR_ERR_LAYOUT),
     (dict(rows=1 << 30, cols=1 << 13, ld=1 << 13, ld_q=1 << 13), abi.BCJR_ERR_SIZE),
+    (dict(rows=(1 << 23) + 1), abi.BCJR_ERR_SIZE),
+    (dict(rows=1 << 23, cols=(1 << 11) + 1, ld=1 << 12, ld_q=1 << 12), abi.BCJR_ERR_SIZE),
     (dict(rows=0), abi.BCJR_OK), (dict(cols=0, ld=0, x=None), abi.BCJR_OK)])
 def test_quantize_refusals(change, status):
     assert quantize(**change) == status
@@ -60,7 +62,9 @@ def test_quantize_refusals(change, status):
     (dict(b_rows=2), abi.BCJR_ERR_SIZE), (dict(m=-1), abi.BCJR_ERR_SIZE), (dict(k=BIG), abi.BCJR_ERR_SIZE),
     (dict(a=P + 4), abi.BCJR_ERR_LAYOUT), (dict(ld_b=40), abi.BCJR_ERR_LAYOUT), (dict(k=17), abi.BCJR_ERR_LAYOUT),
     (dict(ld_out=7), abi.BCJR_ERR_LAYOUT), (dict(ld_a=1 << 31), abi.BCJR_ERR_LAYOUT),
-    (dict(m=1 << 30, n=1 << 30, ld_out=1 << 30), abi.BCJR_ERR_SIZE), (dict(m=0), abi.BCJR_OK), (dict(n=0), abi.BCJR_OK)])
+    (dict(m=1 << 30, n=1 << 30, ld_out=1 << 30), abi.BCJR_ERR_SIZE),
+    (dict(m=1 << 23, n=(1 << 14) + 1, ld_out=1 << 15), abi.BCJR_ERR_SIZE),
+    (dict(k=16, ld_a=(1 << 23) + 16), abi.BCJR_ERR_LAYOUT), (dict(m=0), abi.BCJR_OK), (dict(n=0), abi.BCJR_OK)])
 def test_matmul_refusals(change, status):
     assert matmul(**change) == status
 
