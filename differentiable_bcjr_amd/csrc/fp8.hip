@@ -58,7 +58,8 @@ __device__ __forceinline__ void store8(uint8_t* p, int count, uint2 w) {
     }
 }
 
-// Rows alone: 16 lanes hold one row's block of 128, eight elements each.  Bound by memory.
+// Rows alone: 16 lanes hold one row's block of 128, eight elements each.  Bound by memory: 8192 x 2048 in bfloat16 take
+// 10 us, 50 MB at 5.0 TB/s (a large copy moves 5.1).
 constexpr int kRowsPerGroup = 16;
 
 template <class T>
@@ -78,7 +79,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantizeArgs a, int 
 
 // A tile of 128 x 128: square blocks, and any quantization that also writes the transpose.  Thread t holds eight
 // columns of eight consecutive rows, so both orientations leave it as words of eight codes; the transposed codes pass
-// through LDS to be written in whole 128-byte lines.
+// through LDS to be written in whole 128-byte lines.  The tile stays in registers as it lies in memory and is converted
+// at each use, which halves its registers in 16-bit types.  8192 x 8192 in bfloat16, both orientations, take 48 us (268 MB
+// at 5.6 TB/s), 8192 x 2048 in float32 with square blocks 16 us (101 MB at 6.3 TB/s, part of it from cache).
 template <class T, bool kSquare, bool kTransposed>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantizeArgs a, int col_blocks, int row_blocks) {
     __shared__ uint32_t col_max[4][128];
@@ -489,7 +492,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * kGroups, 2) void product_k
 // whole 64-byte sectors), the workgroup's waves share the slabs of those rows among them, and their sums meet in LDS in
 // a fixed order.  All loads of the slabs that a wave takes at a time are issued before the first is used.  a (up to 16
 // rows for each of kTiles fragments) comes as codes; or, where it is small, as numbers, which every workgroup quantizes
-// into its LDS while its first rows of b are on their way.
+// into its LDS while its first rows of b are on their way.  One token against 8192 x 2048: 5.2 us either way (16.8 MB at
+// 3.2 TB/s, about 2.5 us of it a launch's own time), where quantizing first would be a second launch of 2.7 us.
 
 __device__ __forceinline__ v8i load_slab(const uint8_t* row, int at, int g, int k) {
     return __builtin_shufflevector(load_chunk(row, at + g * 16, k), load_chunk(row, at + 64 + g * 16, k), 0, 1, 2, 3, 4,
@@ -629,11 +633,10 @@ template <class T, class X, int kTiles>
 void few_rows(const ProductArgs& a, hipStream_t st) {
     const int slabs = (a.k + kSlab - 1) / kSlab;
     const unsigned grid = (unsigned)((a.n + 15) / 16);
-    // Waves so that each takes about four slabs at once; with fewer workgroups than compute units, so that each takes
-    // one: then it is latency that counts.
-    const int per = grid < 256 ? 1 : 4;
+    // Waves so that each takes about four slabs, all of whose loads it issues at once: one token against 8192 x 2048
+    // 5.2 us, with a slab a wave 6.7 us.
     int waves = 1;
-    while (waves < 16 && waves * per < slabs) waves *= 2;
+    while (waves < 16 && waves * 4 < slabs) waves *= 2;
     if (a.b_rows == 1)
         few_rows_kernel<T, X, kTiles, true><<<grid, waves * 64, 0, st>>>(a);
     else
@@ -654,20 +657,40 @@ void product_tiles(const ProductArgs& a, hipStream_t st) {
     product_kernel<T, BM, BN, WAVES_M, WAVES_N, kStages, kGroups, false><<<grid, kThreads, 0, st>>>(a, tm, tn);
 }
 
+// Few rows: 16 against 2048 x 8192 take 10 us here and 18 us in tiles of 64, 32 take 12 and 18 us, 40 would take 20 and
+// 18 us.  Otherwise the largest tiles that leave no compute unit idle; in microseconds, for a 16-bit result with square
+// blocks (8-bit MFMAs) and a float32 one with a scale for each row of both (16-bit MFMAs):
+//                              256 x 256   256 x 128   128 x 128   64 x 64
+//   8192 x 8192 x 2048, 16-bit       146         173         157       303
+//   4096 x 2048 x 2048, 16-bit        37          25          25        40
+//   2048 x 2048 x 2048, 16-bit        34          22          18        21
+//   8192 x 2048 x 8192, float32        -         343         362       478
+//   2048 x 2048 x 2048, float32        -          40          30        34
+// (256 x 256 holds no float32 kernel's widened operands, nor a scale for each of its columns, in registers.)  Where
+// tiles of 64 do not fill the card, two groups of waves share a tile's k loop: 1000 x 512 x 2048 8.9 to 7.5 us, 100 x
+// 512 x 8192 25 to 18 us.
+//
+// 8192 x 8192 x 2048 runs at 1.9 PFLOP/s; hipBLASLt reaches 2.45 with one scale for the whole matrix.  At 2.1 GHz (the
+// clock that the power limit leaves) the matrix cores are busy 43% of it and the vector unit, with the scaling
+// multiply-adds, 32%; without its loads the kernel takes 137 us, without the first fragments' LDS reads 141 us.  The
+// float32 product is bound by the vector unit, which widens each code for two fragments' MFMAs.
 template <class T>
 hipError_t product(const ProductArgs& a, hipStream_t st) {
+    constexpr bool kFloat = sizeof(T) == 4;
+    constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
     if (a.m <= 16) {
         few_rows<T, uint8_t, 1>(a, st);
     } else if (a.m <= kFewCodedRows) {
         few_rows<T, uint8_t, 2>(a, st);
-    } else if (sizeof(T) == 2 && a.b_rows == 128 && tiles(256, 256) >= 256) {
-        if constexpr (sizeof(T) == 2) product_tiles<T, 256, 256, 2, 4, 2, 1, false>(a, st);
-    } else if (tiles(256, 128) >= 256) {
-        product_tiles<T, 256, 128, 4, 2, 3, 1>(a, st);
-    } else if (tiles(128, 128) >= 256) {
+    } else if (kFloat ? tiles(256, 128) >= kCus : a.b_rows == 128 && tiles(256, 256) >= kCus) {
+        if constexpr (kFloat)
+            product_tiles<T, 256, 128, 4, 2, 3, 1>(a, st);
+        else
+            product_tiles<T, 256, 256, 2, 4, 2, 1, false>(a, st);
+    } else if (tiles(128, 128) >= kCus) {
         product_tiles<T, 128, 128, 2, 2, 2, 1>(a, st);
-    } else if (tiles(64, 64) <= 256 && a.k >= 8 * kSlab) {
+    } else if (tiles(64, 64) <= kCus && a.k >= 8 * kSlab) {
         product_tiles<T, 64, 64, 2, 2, 4, 2>(a, st);
     } else {
         product_tiles<T, 64, 64, 2, 2, 4, 1>(a, st);

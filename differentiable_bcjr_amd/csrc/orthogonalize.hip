@@ -6,11 +6,14 @@
 // and transposed, so that every product reads both operands along their rows; A and B are symmetric and held scaled by
 // 2^8.  The scales keep the entries of a normalised matrix (rms (m n)^-1/2) far from the halves' subnormal range and
 // leave room for |X| < 64 and |A|, |B| < 256.  The products run on the 16-bit matrix instructions with float32 sums.
-// For a bfloat16 result they take the hi halves alone: each product then rounds its operands to 11 bits, while X itself
-// keeps its 22 through a X, which carries the small singular values (rounding X to 11 bits in every step loses them:
-// on a rank-16 matrix with 1% noise the result is 4e-2 off; with X kept it is 4e-4, below the 1.7e-3 of rounding the
-// result to bfloat16).  For a float32 or float16 result each product is hi hi + hi lo + lo hi, three times the work,
-// and the result is as near the exact one as that of float32 products.
+// For a bfloat16 result of more than 256 rows they take the hi halves alone: each product then rounds its operands to 11
+// bits, while X itself keeps its 22 through a X, which carries the small singular values (rounding X to 11 bits in every
+// step loses them: on a rank-16 matrix with 1% noise the result is 4e-2 off; with X kept it is 4e-4, below the 1.7e-3 of
+// rounding the result to bfloat16).  The last step, whose errors no other step follows, takes (a + mu) X + (B - mu I) X
+// with mu = b + c, B's diagonal where the rows of X are orthonormal: what is rounded is then mostly small (1.4e-3 to
+// 1.1e-3 at 512 x 512).  Fewer rows take little more than their launches either way and are hurt most (2.7e-3 at 16 x
+// 300), so they and float32 and float16 results take hi hi + hi lo + lo hi, three times the work, and come as near the
+// exact result as float32 products do.
 #include "bcjr.h"
 
 #include <algorithm>
@@ -25,6 +28,7 @@ namespace {
 constexpr float kXScale = 1024.0f;
 constexpr float kAScale = 256.0f;
 constexpr int kPad = 64;        // rows and columns of X are padded with zeros to multiples of it
+constexpr int kSplitRows = 256; // up to so many rows of X every product is of both halves
 constexpr int kPartials = 256;  // partial sums of |G|^2 per matrix
 
 __host__ __device__ inline int64_t pad_up(int64_t v) { return (v + kPad - 1) / kPad * kPad; }
@@ -149,6 +153,12 @@ __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows
 
 // ---------------------------------------------------------------- the products
 //
+// What bounds them, 8192 x 2048 with a float32 result: a X + B X (206 GFLOP in its three products) takes 185 to 205 us, of
+// which about 40 us are the 200 MB that its ending reads and writes (X, and X again and X^T), exposed because one
+// workgroup fills a compute unit; X X^T 104 + 17 us for 116 GFLOP (75 us of the 104 without any
+// load from memory).  The card holds 2.1 GHz under them.  Tiles of 128, two workgroups to a compute unit, would overlap endings with products but read
+// the operands twice as often: 228 us against 208.
+//
 // Operands: with kSplit a row holds, for each 32 columns, the 32 hi halves and then the 32 lo halves, so one slab brings
 // both halves of 32 columns and its three products are formed from the same two fragments; without, a row holds the hi
 // halves alone (and X's lo halves lie in an array of their own).  The symmetric products compute the tiles on and below
@@ -175,6 +185,7 @@ struct ProdArgs {
     _Float16* t;                  // its transpose [cols][rows]: the same array where it is symmetric
     int64_t o_batch, lo_batch;
     float alpha, beta;            // kGram: alpha acc; kPoly, kStep: alpha old + beta acc
+    float shift;                  // kPoly: subtracted on the diagonal
     void* out;                    // kStep, last: the result in its own type, m x n or (tall) n x m
     int32_t m, n, tall;
     int64_t out_batch;
@@ -246,6 +257,8 @@ __device__ __forceinline__ void finish(const ProdArgs& a, v4f (&acc)[TM][TN], in
                     float x = (float)hi[i][j][e];
                     if constexpr (kSplit || kMode == kStep) x += (float)lo[i][j][e];
                     acc[i][j][e] = fmaf(a.alpha, x, a.beta * acc[i][j][e]);
+                    if constexpr (kMode == kPoly)
+                        if (row0 + i * 16 + r16 == col0 + j * 16 + g * 4 + e) acc[i][j][e] -= a.shift;
                 }
     }
     forget();
@@ -563,6 +576,8 @@ hipError_t iterate(const OrthoArgs& o, const Layout& l, hipStream_t st) {
         poly.o_batch = s_batch;
         poly.alpha = o.b;
         poly.beta = o.c / kAScale;
+        const float mu = !kSplit && s + 1 == o.steps ? o.b + o.c : 0.0f;
+        poly.shift = mu * kAScale;
         poly.partial = (float*)(ws + l.sums);
         launch_product<kPoly, kSplit, float>(poly, o.batch, st);
 
@@ -579,7 +594,7 @@ hipError_t iterate(const OrthoArgs& o, const Layout& l, hipStream_t st) {
         step.lo_batch = l.mp * l.np;
         step.t = at(l.xt[next]);
         step.o_batch = x_batch;
-        step.alpha = o.a;
+        step.alpha = o.a + mu;
         step.beta = 1.0f / kAScale;
         step.m = (int32_t)l.m;
         step.n = (int32_t)l.n;
@@ -611,7 +626,8 @@ hipError_t orthogonalize_from(const OrthoArgs& o, hipStream_t st) {
                                                           parts, o.eps, direct, turned, at(l.x_lo), l.tall, rp, cp);
     switch (o.out_type) {
         case BCJR_TYPE_F32: return iterate<true, float>(o, l, st);
-        case BCJR_TYPE_BF16: return iterate<false, __hip_bfloat16>(o, l, st);
+        case BCJR_TYPE_BF16:
+            return l.split ? iterate<true, __hip_bfloat16>(o, l, st) : iterate<false, __hip_bfloat16>(o, l, st);
         default: return iterate<true, _Float16>(o, l, st);
     }
 }
@@ -627,7 +643,7 @@ Layout make_layout(int64_t batch, int64_t rows, int64_t cols, int32_t out_type) 
     l.n = l.tall ? rows : cols;
     l.mp = pad_up(l.m);
     l.np = pad_up(l.n);
-    l.split = out_type != BCJR_TYPE_BF16;
+    l.split = out_type != BCJR_TYPE_BF16 || l.mp <= kSplitRows;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;

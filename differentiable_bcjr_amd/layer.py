@@ -260,8 +260,8 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
                   out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """The matrices of g [..., rows, cols] with their singular values brought near 1, by ``steps`` Newton-Schulz steps
     X <- a X + (b A + c A A) X, A = X X^T, from X = g / (|g|_F + eps) (on the transpose where rows > cols).  The result
-    has g's type or ``out_dtype``: float32 and float16 are computed like float32 products, bfloat16 with operands
-    rounded to 11 bits."""
+    has g's type or ``out_dtype``: float32 and float16 are computed like float32 products, bfloat16 of more than 256 rows
+    and columns with operands rounded to 11 bits."""
     if not isinstance(g, torch.Tensor) or not g.is_cuda:
         raise TypeError("g must be a CUDA (HIP) tensor")
     in_type, out_dtype = _type(g.dtype, "g"), out_dtype or g.dtype

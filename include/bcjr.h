@@ -357,8 +357,9 @@ size_t fp8_linear_quantized_workspace_bytes(int64_t m, int64_t k);
  * on the transpose when G has more rows than columns.  With a, b, c = 3.4445, -4.7750, 2.0315 five steps bring the
  * singular values near 1.  g is [batch][rows, cols] of `type`, rows ld_g and matrices batch_g elements apart; out is
  * contiguous, of out_type.  Sums are float32 (|G|_F: float64).  A float32 or float16 result is as near the exact
- * iteration as one of float32 products; a bfloat16 result comes from products of operands rounded to 11 bits, whose
- * error is below that of the result's own rounding.  The iterates must stay below 64 in |X| and 256 in |A| and
+ * iteration as one of float32 products, and so is a bfloat16 one of up to 256 rows or columns before its rounding; a
+ * larger bfloat16 result comes from products of operands rounded to 11 bits, whose error is below that of the result's
+ * own rounding.  The iterates must stay below 64 in |X| and 256 in |A| and
  * |b A + c A A| (the usual coefficients keep them under 3); beyond that the result has Inf or NaN entries.  A NaN or Inf
  * in G makes that matrix's result NaN.  1 <= steps <= 1000, 1 <= batch <= 65535, rows, cols <= 65536.
  * Workspace: orthogonalize_workspace_bytes, 256-byte aligned (BCJR_ERR_WORKSPACE).

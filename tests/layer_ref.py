@@ -65,7 +65,7 @@ def newton_schulz(g, steps, coefficients, eps):
 
 def newton_schulz_rounded(g, steps, coefficients, eps, split):
     """The iteration with float32 products of operands rounded as the library documents: to the sum of two halves
-    (split), or to one half with X itself kept as the sum of two."""
+    (split), or to one half with X itself kept as the sum of two and b + c taken off B's diagonal in the last step."""
     a, b, c = coefficients
 
     def half(v):
@@ -81,8 +81,9 @@ def newton_schulz_rounded(g, steps, coefficients, eps, split):
     x = two((x / (x.square().sum().sqrt() + eps)).float() * 1024)
     for i in range(steps):
         s = op(op(x) @ op(x).t() * (256 / 1024 ** 2))
-        p = op(b * s + s @ s * (c / 256))
-        x = a * x + p @ op(x) * (1 / 256)
+        mu = 0.0 if split or i + 1 < steps else b + c
+        p = op(b * s + s @ s * (c / 256) - mu * 256 * torch.eye(s.shape[0]))
+        x = (a + mu) * x + p @ op(x) * (1 / 256)
         x = two(x) if i + 1 < steps else x
     x = x / 1024
     return x.t() if tall else x

@@ -423,7 +423,8 @@ def _check_orthogonal(got, g, steps, coefficients, eps, out_dtype):
     """Against 64 bits.  The bound is four times what the documented roundings alone make of this matrix (emulated on
     the CPU with float32 products), and the rounding of the result."""
     r = ref.newton_schulz(g, steps, coefficients, eps)
-    emulated = ref.newton_schulz_rounded(g, steps, coefficients, eps, out_dtype != torch.bfloat16).double()
+    split = out_dtype != torch.bfloat16 or min(g.shape) <= 256
+    emulated = ref.newton_schulz_rounded(g, steps, coefficients, eps, split).double()
     off, norm = float((emulated - r).norm()), float(r.norm())
     err = float((got.cpu().double() - r).norm())
     tiny = torch.finfo(out_dtype).tiny * torch.finfo(out_dtype).eps * math.sqrt(r.numel())
@@ -433,7 +434,7 @@ def _check_orthogonal(got, g, steps, coefficients, eps, out_dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 300), (300, 1), (7, 5), (16, 16), (64, 64), (65, 130), (128, 128),
-                                       (200, 100), (129, 1000), (520, 300), (50, 4200), (8300, 60), (130, 4100)])
+                                       (200, 100), (129, 1000), (520, 300), (260, 257), (400, 1100), (50, 4200), (8300, 60), (130, 4100)])
 def test_orthogonalize_sizes(dev, rows, cols, dtype):
     g = _update("plain", rows, cols, rows + cols).to(dtype)
     _check_orthogonal(dba.orthogonalize(g.to(dev)), g.float(), 5, USUAL, 1e-7, dtype)
@@ -441,7 +442,7 @@ def test_orthogonalize_sizes(dev, rows, cols, dtype):
 
 @pytest.mark.parametrize("out_dtype", TYPES)
 @pytest.mark.parametrize("kind", ["low-rank", "one-entry", "large"])
-@pytest.mark.parametrize("rows,cols", [(96, 200), (257, 130)])
+@pytest.mark.parametrize("rows,cols", [(96, 200), (257, 130), (300, 420)])
 def test_orthogonalize_kinds(dev, rows, cols, kind, out_dtype):
     g = _update(kind, rows, cols, 9)
     _check_orthogonal(dba.orthogonalize(g.to(dev), out_dtype=out_dtype), g, 5, USUAL, 1e-7, out_dtype)

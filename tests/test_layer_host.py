@@ -131,10 +131,12 @@ def test_orthogonalize_refusals(change, status):
 
 def test_orthogonalize_workspace():
     size = abi.orthogonalize_workspace_bytes
-    # X as two halves and its transpose twice, A and B; a float32 result keeps the second half of the rest too
+    # X as two halves and its transpose twice, A and B; up to 256 rows and for a float32 result both halves of all
+    x, s = 320 * 448 * 2, 320 * 320 * 2
+    assert size(1, 300, 400, abi.BCJR_TYPE_BF16) == 256 * 8 + 4 * x + 2 * s
+    assert size(1, 300, 400, abi.BCJR_TYPE_F32) == 256 * 8 + 6 * x + 4 * s
     x, s = 128 * 192 * 2, 128 * 128 * 2
-    assert size(1, 100, 150, abi.BCJR_TYPE_BF16) == 256 * 8 + 4 * x + 2 * s
-    assert size(1, 100, 150, abi.BCJR_TYPE_F32) == 256 * 8 + 6 * x + 4 * s
+    assert size(1, 100, 150, abi.BCJR_TYPE_BF16) == size(1, 100, 150, abi.BCJR_TYPE_F32) == 256 * 8 + 6 * x + 4 * s
     assert size(1, 150, 100, abi.BCJR_TYPE_F32) == size(1, 100, 150, abi.BCJR_TYPE_F32)
     assert size(3, 64, 64, abi.BCJR_TYPE_F16) == 3 * size(1, 64, 64, abi.BCJR_TYPE_F32)
     for bad in ((0, 8, 8, 0), (1, 0, 8, 0), (1, 8, 65537, 0), (1, 8, 8, 3)):
