@@ -679,16 +679,23 @@ hipError_t product(const ProductArgs& a, hipStream_t st) {
     constexpr bool kFloat = sizeof(T) == 4;
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
+    // Whether tiles fill the card and, with what they hold beyond the edges, are not much more work than smaller ones: a
+    // quarter at most (300 x 65536 x 512 24 us, in tiles of 256 27 us), half where the smaller ones are of 64 (130 x
+    // 16384 x 2048 18 us, in tiles of 64 21 us).
+    const auto large = [&](int64_t bm, int64_t bn, int64_t small) {
+        return tiles(bm, bn) >= kCus &&
+               tiles(bm, bn) * bm * bn * 4 <= tiles(small, small) * small * small * (small == 64 ? 6 : 5);
+    };
     if (a.m <= 16) {
         few_rows<T, uint8_t, 1>(a, st);
     } else if (a.m <= kFewCodedRows) {
         few_rows<T, uint8_t, 2>(a, st);
-    } else if (kFloat ? tiles(256, 128) >= kCus : a.b_rows == 128 && tiles(256, 256) >= kCus) {
+    } else if (kFloat ? large(256, 128, 128) : a.b_rows == 128 && large(256, 256, 128)) {
         if constexpr (kFloat)
             product_tiles<T, 256, 128, 4, 2, 3, 1>(a, st);
         else
             product_tiles<T, 256, 256, 2, 4, 2, 1, false>(a, st);
-    } else if (tiles(128, 128) >= kCus) {
+    } else if (large(128, 128, 64)) {
         product_tiles<T, 128, 128, 2, 2, 2, 1>(a, st);
     } else if (tiles(64, 64) <= kCus && a.k >= 8 * kSlab) {
         product_tiles<T, 64, 64, 2, 2, 4, 2>(a, st);

@@ -525,10 +525,17 @@ inline Cut cut_product(int64_t batch, int64_t rows, int64_t cols, int64_t k, boo
     };
     constexpr int64_t kCus = 256;
     const int64_t slabs = k / slab_cols;
-    if (tiles(256) >= kCus * 3 / 4) return {256, 1, 1};
-    if (symmetric && tiles(256) >= 24 && slabs >= 64) return {256, (int)std::max<int64_t>(1, kCus / tiles(256)), 1};
-    if (tiles(128) > kCus) return {128, 1, 1};
-    if (tiles(128) >= kCus / 2 && slabs >= 4) return {128, 1, 2};
+    // whether what tiles hold beyond the edges makes them not much more work than tiles of 64 (260 matrices of 64 x 64 in
+    // float32 take 99 us, in tiles of 256, which they would fill the card with, 307 us)
+    const auto fits = [&](int64_t size) { return tiles(size) * size * size * 2 <= tiles(64) * 64 * 64 * 3; };
+    if (fits(256)) {
+        if (tiles(256) >= kCus * 3 / 4) return {256, 1, 1};
+        if (symmetric && tiles(256) >= 24 && slabs >= 64) return {256, (int)std::max<int64_t>(1, kCus / tiles(256)), 1};
+    }
+    if (fits(128)) {
+        if (tiles(128) > kCus) return {128, 1, 1};
+        if (tiles(128) >= kCus / 2 && slabs >= 4) return {128, 1, 2};
+    }
     if (symmetric && tiles(64) <= kCus / 4 && slabs >= 64)
         return {64, (int)std::min(kCus / tiles(64), slabs / 16), 1};
     return {64, 1, tiles(64) <= kCus && slabs >= 4 ? 2 : 1};
