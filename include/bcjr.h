@@ -341,7 +341,7 @@ size_t fp8_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
 /*
  * The layer of a served model: out [m, n] = x w^T in x's type, for weights w [n, k] quantized before (w_scale and
  * w_block_rows as b's above) and x [m, k] of `type`, quantized on the way as fp8_block_quantize does with
- * block_rows = 1.  The result is fp8_block_matmul's of those codes up to the order of its float32 sums.  Up to 4 rows
+ * block_rows = 1.  The result is fp8_block_matmul's of those codes up to the order of its float32 sums.  Up to 16 rows
  * of up to 32768 numbers in all take one launch and no workspace; more take two and
  * fp8_linear_quantized_workspace_bytes(m, k) bytes, 256-byte aligned (BCJR_ERR_WORKSPACE).
  */

@@ -235,7 +235,8 @@ def test_linear_and_gradients_are_the_formulas(dev, m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,n,k", LINEAR + [(2, 2048, 512), (33, 70, 8192), (40, 64, 100), (4, 40, 8192),
-                                           (3, 4200, 1000), (4, 50, 8300), (1, 33, 33000)])
+                                           (3, 4200, 1000), (4, 50, 8300), (1, 33, 33000), (16, 100, 2048),
+                                           (15, 4200, 2100), (16, 60, 2050), (9, 20, 3500)])
 def test_linear_quantized_is_quantize_then_matmul(dev, m, n, k, dtype):
     x, w, _ = _linear_case(m, n, k, dtype, seed=m + n + k)
     for block_rows in (1, 128):

@@ -111,7 +111,8 @@ def test_linear_buffers():
     assert ws(m, n, k) == max(forward_ws, backward_ws)
     assert abi.fp8_linear_quantized_workspace_bytes(4, 8192) == abi.fp8_linear_quantized_workspace_bytes(1, 32768) == 0
     assert abi.fp8_linear_quantized_workspace_bytes(4, 8193) == up(4 * 8208) + up(4 * 65 * 4)
-    assert abi.fp8_linear_quantized_workspace_bytes(5, k) == up(5 * 48) + up(5 * 4)
+    assert abi.fp8_linear_quantized_workspace_bytes(16, 2048) == 0
+    assert abi.fp8_linear_quantized_workspace_bytes(17, k) == up(17 * 48) + up(17 * 4)
     assert abi.fp8_linear_quantized_workspace_bytes(m, k) == up(m * 48) + up(m * 4)
     assert saved(-1, n, k, 3) == ws(m, BIG, k) == abi.fp8_linear_quantized_workspace_bytes(-1, k) == 0
 
