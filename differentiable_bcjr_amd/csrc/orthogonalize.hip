@@ -108,7 +108,8 @@ __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows
     const int t = threadIdx.x;
     const int64_t item = blockIdx.z;
     const double total = block_sum(t < parts ? partials[item * kPartials + t] : 0.0, lds);
-    const float norm = (float)(sqrt(total) + (double)eps);
+    // in 64 bits, as the norm of entries near float32's largest is beyond it and that of subnormal ones has no reciprocal
+    const double scale = (double)kXScale / (sqrt(total) + (double)eps);
     const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
     const T* p = g + item * batch_stride;
     const int64_t base = item * rows_p * cols_p;
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(256) void normalize_kernel(const T* g, int64_t rows
 #pragma unroll
     for (int j = 0; j < 16; ++j) {   // what lies outside G stays 0, also where the norm is 0 or NaN
         _Float16 hi, lo;
-        split(j < left ? v[j / 8].at(j % 8) / norm * kXScale : 0.0f, hi, lo);
+        split(j < left ? (float)((double)v[j / 8].at(j % 8) * scale) : 0.0f, hi, lo);
         w[j] = (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
     }
     put(direct, r0 + line, cols_p, c0 + q, w, !tall);

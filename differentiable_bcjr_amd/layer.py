@@ -93,7 +93,8 @@ def fp8_block_quantize(x: torch.Tensor, *, block_rows: int = 1, transposed: bool
     [ceil(M / block_rows), ceil(K / 128)], one for each block of 128 columns of one row (``block_rows=1``, activations
     and gradients) or of 128 rows (``block_rows=128``, weights).  q scale stands for x, with scale = amax / 448 (at
     least 2^-126).  With ``transposed`` also (q_t [K, M], scale_t [ceil(K / block_rows), ceil(M / 128)]) of the
-    transpose, from the same pass over x.  An Inf or NaN makes the values of its block NaN."""
+    transpose, from the same pass over x.  An Inf or NaN makes the values of its block NaN.  Neither
+    the codes nor the scales carry a gradient."""
     x, x_type, rows, cols, ld = _matrix(x, "x")
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
@@ -187,9 +188,11 @@ def _tokens(x, k: int, w: torch.Tensor):
 
 def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor) -> torch.Tensor:
     """y [..., N] = x w^T in x's type, for weights w [N, K] quantized before (``fp8_block_quantize(weights,
-    block_rows=128)``); x [..., K] is quantized on the way, a scale for each 128 of a row."""
+    block_rows=128)``); x [..., K] is quantized on the way, a scale for each 128 of a row.  It has no gradient (``fp8_linear`` has): an x that asks for
+    one is refused unless gradients are off."""
     w, n, k, ld_w, w_scale, b_rows = _weights(w, w_scale, "w")
     rows, x_type, m, _, ld_x = _tokens(x, k, w)
+    _no_gradient(x, "fp8_linear_quantized")
     dev, lib = w.device, _entry()
     y = torch.empty((m, n) if x.dim() == 2 else (*x.shape[:-1], n), dtype=x.dtype, device=dev)
     need = lib.fp8_linear_quantized_workspace_bytes(m, k)
@@ -197,6 +200,11 @@ def fp8_linear_quantized(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor
     _call(lib.fp8_linear_quantized, dev.index, rows.data_ptr(), x_type, m, ld_x, w.data_ptr(), ld_w, w_scale.data_ptr(),
           b_rows, n, k, y.data_ptr(), n or 1, _ptr(ws), need)
     return y
+
+
+def _no_gradient(x, name: str) -> None:
+    if x.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad() or on a detached tensor")
 
 
 def _bytes(n: int, device) -> torch.Tensor | None:
@@ -261,13 +269,15 @@ def orthogonalize(g: torch.Tensor, *, steps: int = 5, coefficients=(3.4445, -4.7
     """The matrices of g [..., rows, cols] with their singular values brought near 1, by ``steps`` Newton-Schulz steps
     X <- a X + (b A + c A A) X, A = X X^T, from X = g / (|g|_F + eps) (on the transpose where rows > cols).  The result
     has g's type or ``out_dtype``: float32 and float16 are computed like float32 products, bfloat16 of more than 256 rows
-    and columns with operands rounded to 11 bits."""
+    and columns with operands rounded to 11 bits.  It has no gradient: a g that asks for one is refused unless gradients
+    are off."""
     if not isinstance(g, torch.Tensor) or not g.is_cuda:
         raise TypeError("g must be a CUDA (HIP) tensor")
     in_type, out_dtype = _type(g.dtype, "g"), out_dtype or g.dtype
     out_type = _type(out_dtype, "out_dtype")
     if g.dim() < 2:
         raise ValueError("g must have at least two dimensions")
+    _no_gradient(g, "orthogonalize")
     a, b, c = (float(v) for v in coefficients)
     out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
     if out.numel() == 0:

@@ -282,6 +282,18 @@ def test_linear_takes_one_token_an_empty_sum_and_a_broadcast_gradient(dev):
         first.sum().backward()
 
 
+def test_calls_without_a_gradient_refuse_to_lose_one(dev):
+    g = _randn(20, 40, seed=1).to(dev)
+    q = dba.fp8_block_quantize(g, block_rows=128)
+    for call in (lambda x: dba.fp8_linear_quantized(x, *q), dba.orthogonalize):
+        want = call(g)
+        asks = g.clone().requires_grad_(True)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            call(asks)
+        with torch.no_grad():
+            assert torch.equal(call(asks), want)
+
+
 def test_linear_step_in_a_graph(dev):
     """Forward and both gradients captured together and replayed on new inputs, against the eager step."""
     x, w, dy = (t.to(dev) for t in _linear_case(70, 140, 150, torch.bfloat16))
@@ -474,6 +486,18 @@ def test_orthogonalize_zero_nan_inf_stay_in_their_matrix(dev):
     got = dba.orthogonalize(g.to(dev))
     assert (got[0] == 0).all() and got[1].isnan().all() and got[3].isnan().all()
     assert torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 120, 2.0 ** -149])
+def test_orthogonalize_over_the_range_of_float32(dev, scale):
+    """A power of two changes nothing without eps, also where |g|_F is beyond float32 or the entries are subnormal."""
+    g = (_update("plain", 300, 420, 5) * 30).round()
+    want = dba.orthogonalize(g.to(dev), eps=0.0)
+    _check_orthogonal(want, g, 5, USUAL, 0.0, torch.float32)
+    scaled = (g.double() * scale).float()
+    assert torch.equal(scaled.double(), g.double() * scale)
+    assert scale < 1 or scaled.norm().isinf()
+    assert torch.equal(dba.orthogonalize(scaled.to(dev), eps=0.0), want)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
