@@ -210,7 +210,8 @@ hipError_t quantize(const QuantizeArgs& a, hipStream_t st) {
 // out[i][j] = sum over blocks B of sa[i][B] sb[j][B] sum over k in B of a[i][k] b[j][k].  A slab is one block, so each
 // MFMA (or four of the 16-bit kind) sums one block of one 16 x 16 tile from zero, and a float32 fused multiply-add with
 // the two scales' product moves it into the running sum.  The MFMA's row operand is b, so a lane holds four neighbouring
-// outputs of one row of a: one scale of a for each 16 rows, and a vector store.
+// outputs of one row of a: one scale of a for each 16 rows, and a vector store.  Against square blocks of b the two scales
+// are multiplied first: blocks whose scales' product is below 2^-126 (x near 1e-31 and w near 1e-3) lose bits of it.
 //
 // The 8-bit instruction aligns the products of eight neighbouring k to the largest of them and drops what lies more than
 // 13 bits below its leading bit (measured: 2^16 + 2^2 gives 2^16 within such a group, and a full float32 sum across

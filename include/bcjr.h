@@ -311,8 +311,9 @@ int fp8_block_quantize(const void* x, int32_t type, int64_t rows, int64_t cols, 
  * sum with one multiplication by its scales.  For a float32 result a block's products are exact and summed in float32.
  * For a bfloat16 or float16 result the 8-bit matrix instruction sums it, which cuts the products of 8 neighbouring k
  * 13 bits below the largest exponent among them (a relative error near 1e-4 on random data, under the result's own
- * rounding).  a and b lie on 16-byte boundaries with ld_a, ld_b multiples of 16
- * up to 2^23 (BCJR_ERR_LAYOUT); bytes behind a row's k codes are not used.
+ * rounding).  With b_block_rows = 128 a block's two scales are multiplied first: a product of theirs below 2^-126 loses
+ * bits, and one beyond 2^128 gives Inf or NaN.  a and b lie on 16-byte boundaries with ld_a, ld_b multiples of 16 up to
+ * 2^23 (BCJR_ERR_LAYOUT); bytes behind a row's k codes are not used.
  */
 int fp8_block_matmul(const void* a, int64_t ld_a, const float* a_scale, const void* b, int64_t ld_b,
                      const float* b_scale, int32_t b_block_rows, int64_t m, int64_t n, int64_t k, void* out,
