@@ -507,9 +507,9 @@ __device__ __forceinline__ v8i load_full_slab(const uint8_t* row, int at, int g)
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Rows that are quantized on the way, and their numbers (rows rounded up to whole blocks): 8 tokens against 2048 x 2048
-// take 9.3 us with their launch, quantized first 13.7 us, 16 against 8192 x 2048 12.2 and 13.7; with twice the numbers 16
-// against 8192 x 4096 would take 25.7 us, quantized first 13.2 us.
+// Rows that are quantized on the way, and their numbers (rows rounded up to whole blocks): 16 tokens against 2048 x 2048
+// take 8.9 us with their launch, quantized first 13.8 us, 16 against 8192 x 2048 12.2 and 13.7; with twice the numbers 16
+// against 8192 x 4096 would take 22.3 us, quantized first 13.3 us.
 constexpr int kFewRows = 16;
 constexpr int kFewNumbers = 32768;
 constexpr int kFewCodedRows = 32;    // rows of codes
@@ -638,9 +638,12 @@ void few_rows(const ProductArgs& a, hipStream_t st) {
     const int slabs = (a.k + kSlab - 1) / kSlab;
     const unsigned grid = (unsigned)((a.n + 15) / 16);
     // Waves so that each takes about four slabs, all of whose loads it issues at once: one token against 8192 x 2048
-    // 5.2 us, with a slab a wave 6.7 us.
+    // 5.2 us, with a slab a wave 6.7 us.  A wave quantizes four blocks at a time; more waves so that they do it twice at
+    // most, and four times where that takes 16 (16 tokens against 2048 x 2048 10.4 to 6.7 us, 4 against 8192 x 2048 7.4
+    // to 6.3; 8 against 8192 x 2048 7.7 us in 8 waves and 9.6 in 16).
+    const int blocks = sizeof(X) > 1 ? a.m * slabs : 0;
     int waves = 1;
-    while (waves < 16 && waves * 4 < slabs) waves *= 2;
+    while (waves < 16 && (waves * 4 < slabs || waves * (waves < 8 ? 8 : 16) < blocks)) waves *= 2;
     if (a.b_rows == 1)
         few_rows_kernel<T, X, kTiles, true><<<grid, waves * 64, 0, st>>>(a);
     else
